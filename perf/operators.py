@@ -175,7 +175,7 @@ def prepare(case, seed):
         s |= {"dn": rand(T, H).to(dt), "dres": rand(T, H).to(dt)}
     if c["what"].startswith("post"):
         s["y"] = (0.3 * rand(T, H) * torch.exp(0.5 * rand(T, 1))).to(dt)
-        s["gate"] = {"none": lambda: None, "h": lambda: 0.5 + 0.3 * rand(H), "t": lambda: torch.sigmoid(rand(T)),
+        s["gate"] = {"none": lambda: None, "h": lambda: 0.5 + 0.3 * rand(H), "t": lambda: torch.sigmoid(rand(T, 1)),
                      "th": lambda: torch.sigmoid(rand(T, H)).to(dt)}[c["gate"]]()
         if c["what"] == "post_next":
             s["w2"] = 1 + 0.2 * rand(H)
@@ -322,10 +322,6 @@ def _form(n, out):
     return {"n": codes, "scale": s}
 
 
-def _wide_gate(gate, kind):
-    return gate.float()[:, None] if kind == "t" else gate.float()
-
-
 def _norm(s):
     c = s["c"]
     what, dt = c["what"], _dt(c["dtype"])
@@ -341,7 +337,7 @@ def _norm(s):
         dx = s["dres"].float() + r * (dh - h * (dh * h).mean(1, keepdim=True))
         return {"dx": dx.to(dt), "dw": (dn * h).double().sum(0).float()}
     y, gate, alpha = s["y"].float(), s["gate"], c["alpha"]
-    gate = 1.0 if gate is None else _wide_gate(gate, c["gate"])
+    gate = 1.0 if gate is None else gate.float()
     if what == "post_bwd":
         dout, r = s["dout"].float(), torch.rsqrt(y.square().mean(1, keepdim=True) + EPS)
         h = y * r
@@ -352,7 +348,7 @@ def _norm(s):
         if c["gate"] == "h":
             out["dgate"] = dg.double().sum(0).float()
         elif c["gate"] == "t":
-            out["dgate"] = dg.sum(1)
+            out["dgate"] = dg.sum(1, keepdim=True)
         elif c["gate"] == "th":
             out["dgate"] = dg.to(dt)
         return out
@@ -506,7 +502,7 @@ def _norm_exact(s):
         return {"dx": leaf["x"].grad + s["dres"].double(), "dw": leaf["w"].grad}
     u = norm(leaf["y"], leaf["w"])
     if "gate" in leaf:
-        u = u * (leaf["gate"].unsqueeze(1) if c["gate"] == "t" else leaf["gate"])
+        u = u * leaf["gate"]
     o = c["alpha"] * leaf["x"] + u
     if what == "post_bwd":
         o.backward(s["dout"].double())
