@@ -341,6 +341,173 @@ qmoe_status qmoe_decode(const qmoe_ffn_desc* d, const float* logits, const void*
                         float* topk_w, void* y_pairs, uint16_t* out_bf16, float* out_f32,
                         void* ws, size_t ws_bytes, void* stream);
 
+/* =====================================================================
+ * Operators around the experts: matrix products in 8-bit floating point
+ * with a scale for each block of 128 (dense, and for the experts of a
+ * routed batch) with the quantizer that feeds them, the router's balance
+ * loss, and the norms before and after a block.  The conventions at the top
+ * of this file hold for them.  Arrays are contiguous.                    */
+
+/* ---------------------------------------------------------------------
+ * qmoe_fp8_quant -- x to OCP e4m3 codes with one fp32 scale per group:
+ *   a = max |v| of the group, s = max(a / 448, 2^-126) (1 for a group of
+ *   zeros), code = e4m3 of v / s, round to nearest even, saturating.
+ *   A group that holds an infinity or a NaN gets the scale NaN and codes 0,
+ *   so that every product that reads it is NaN.
+ * x: bf16 or fp32 (dtype).  act = 0: [M, K] ([B, M, K] with block);
+ *   act = 1: [M, 2K], v = SiLU(x[m, c]) * x[m, K + c] in fp32.
+ * block = 0 (B must be 1): groups of 128 along a row and/or a column:
+ *   codes   [M, Kp]  with scale   [Kp/128, M], groups along the row;
+ *   codes_t [K, Mp]  with scale_t [Mp/128, K], the transpose, groups along
+ *                    the column of x;
+ * block = 1 (weights; act must be 0): one scale per 128 x 128 block:
+ *   codes   [B, M, Kp] with scale   [B, Mp/128, Kp/128];
+ *   codes_t [B, K, Mp] with scale_t [B, Kp/128, Mp/128];
+ *   Kp and Mp are K and M rounded up to a multiple of 128; codes behind K
+ *   (behind M in codes_t) are written as 0.
+ * Either pair may be NULL, not both.  codes, codes_t: 16-byte aligned.
+ * Limits: B <= 65535, M <= 65535 * 128, K <= 2^30 (QMOE_ERR_UNSUPPORTED). */
+qmoe_status qmoe_fp8_quant(const void* x, int32_t dtype, int32_t B, int32_t M, int32_t K,
+                           int32_t block, int32_t act, uint8_t* codes, float* scale,
+                           uint8_t* codes_t, float* scale_t, void* stream);
+
+/* ---------------------------------------------------------------------
+ * qmoe_fp8_matmul -- out[m,n] = sum_j sa[j,m] * sb(j,n) *
+ *                      sum_{i<128} a[m,128j+i] * b[n,128j+i]
+ * a [M, K] e4m3 codes with a_scale [K/128, M]; b [N, K] with b_scale
+ *   [ceil(N/128), K/128] (b_block = 1: weights) or [K/128, N] (b_block = 0).
+ * out [M, N] bf16 or fp32 (out_dtype).  K % 128 == 0; any M and N.
+ * The products of a K block are summed by the matrix cores, scaled once in
+ * fp32 and added to an fp32 sum, K blocks in order; where the work is split
+ * along K (rules on the sizes) the parts are added in order, so a call gives
+ * the same bits every time.  bf16 outputs take the fp8 matrix instruction,
+ * whose sum of a K block is about 1.4e-5 off (2-norm; far below the output's
+ * rounding); fp32 outputs widen the codes to bf16 and take the bf16
+ * instruction, whose products are exact and summed in fp32.
+ * The three products of a linear layer y = x w^T: forward x, w as they are;
+ * dx = dy . w with codes_t of w (b_block = 1); dw = dy^T . x with codes_t of
+ * dy and of x (b_block = 0).
+ * ws: qmoe_fp8_matmul_workspace(M, N, K) bytes (0: none needed, ws may be
+ *   NULL), 256-byte aligned, contents need no initialisation; calls that
+ *   share it must be ordered on one stream.  a, b: 16-byte aligned.
+ * Limits: M, N, K <= 2^24 (QMOE_ERR_UNSUPPORTED).                        */
+size_t qmoe_fp8_matmul_workspace(int32_t M, int32_t N, int32_t K);
+qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_t* b,
+                            const float* b_scale, int32_t b_block, int32_t M, int32_t N,
+                            int32_t K, void* out, int32_t out_dtype, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* ---------------------------------------------------------------------
+ * qmoe_fp8_grouped_matmul -- the same product for every (token, slot) pair
+ * p with its expert's matrix: out[p] = a[row(p)] . b[expert(p)]^T.
+ * a: pair_rows = 0: [T, K], row(p) = p / k (the first projection);
+ *    pair_rows = 1: [T*k, K], row(p) = p (the second one); a_scale
+ *    [K/128, rows of a].
+ * b [E, N, K] with b_scale [E, ceil(N/128), K/128].
+ * sorted_pair_ids, tile_expert, num_padded: qmoe_align's outputs for the
+ *   same T, k, E and block_m.  out [T*k, N] bf16 or fp32; rows of pairs that
+ *   qmoe_align dropped are left as they are.
+ * K % 128 == 0, any N; E <= 1024.                                        */
+qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int32_t pair_rows,
+                                    const uint8_t* b, const float* b_scale,
+                                    const int32_t* sorted_pair_ids, const int32_t* tile_expert,
+                                    const int32_t* num_padded, int32_t T, int32_t k, int32_t E,
+                                    int32_t block_m, int32_t N, int32_t K, void* out,
+                                    int32_t out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------
+ * qmoe_balance -- the router's balance loss and per-expert counts.  With p
+ * the softmax of a token's logits over the E experts and n the kept tokens:
+ *   counts[e] = picks of e in topk_ids of the kept tokens (ids outside
+ *               [0,E) are not counted; an id repeated in a token counts as
+ *               often as it stands there)
+ *   probs[e]  = sum_t p[t,e] / n
+ *   loss      = coef * E * sum_e counts[e] / (k n) * probs[e]
+ *   tokens    = n
+ * mask: optional [T] bytes, 0 drops a token (its logits and ids are not
+ *   used); NULL keeps all.  n = 0 gives loss 0 and probs 0.  A logit of -inf
+ *   has probability 0; a row of -inf alone has probability 0 everywhere (it
+ *   is still a kept token); NaN or +inf in a kept row makes the loss NaN.
+ * logits fp32 [T,E]; topk_ids int32 [T,k]; loss fp32 [1], counts int32 [E],
+ *   probs fp32 [E], tokens int32 [1].  k <= 16, E <= 1024.
+ * ws: qmoe_balance_workspace(T, E) bytes, 256-byte aligned, contents need no
+ *   initialisation; calls that share it must be ordered on one stream.
+ * qmoe_balance_backward -- the gradient of the loss to the logits, for the
+ * counts and tokens of the forward call (the counts carry none):
+ *   dlogits[t,e] = dloss * coef * E / n * p[t,e] * (f_e - sum_j f_j p[t,j]),
+ *   f_e = counts[e] / (k n); zeros for dropped tokens.  dloss fp32 [1] on
+ *   the device; dlogits fp32 [T,E], written whole (it may be logits).      */
+size_t qmoe_balance_workspace(int32_t T, int32_t E);
+qmoe_status qmoe_balance(const float* logits, const int32_t* topk_ids, const uint8_t* mask,
+                         int32_t T, int32_t E, int32_t k, float coef, float* loss,
+                         int32_t* counts, float* probs, int32_t* tokens, void* ws,
+                         size_t ws_bytes, void* stream);
+qmoe_status qmoe_balance_backward(const float* logits, const uint8_t* mask, const int32_t* counts,
+                                  const int32_t* tokens, const float* dloss, int32_t T, int32_t E,
+                                  int32_t k, float coef, float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------
+ * Norms before and after a block, with its gate and the residual scale.
+ * norm(v) = v / sqrt(mean(v^2) + eps) * w over the H columns, in fp32.
+ * Activations are bf16 or fp32 (dtype, one for all of a call's [T,H]
+ * arrays), w fp32 [H].  eps > 0.  H <= 16384, and <= 8192 where H % 8 != 0
+ * or an array of H columns is not 16-byte aligned (QMOE_ERR_UNSUPPORTED).
+ *
+ * Forms in which a norm is written:
+ *   QMOE_FORM_BF16, QMOE_FORM_F32: n [T,H], scale unused (NULL);
+ *   QMOE_FORM_INT8, QMOE_FORM_E4M3: codes [T,H] with one fp32 scale per
+ *     token, scale [T]: x and x_scale of the grouped FFN's schemes;
+ *   QMOE_FORM_E4M3_B128: codes [T,Hp], scale [Hp/128, T]: qmoe_fp8_quant's
+ *     row form, the a of the products above.
+ * The scale is max(absmax / qmax, 2^-126), qmax 127 or 448 (1 for zeros; NaN
+ * with codes 0 where the group is not finite).
+ *
+ * qmoe_pre_norm -- n = norm(x).
+ * qmoe_post_norm -- out = alpha * x + g * norm(y): y the block's output, x
+ *   the residual stream, g the gate (QMOE_GATE_NONE: 1; COLUMN: fp32 [H];
+ *   TOKEN: fp32 [T]; FULL: [T,H] in dtype).  With next_w it also writes n,
+ *   the norm of the stored out with the weights next_w, in `form`: the same
+ *   bits as qmoe_pre_norm of out.  out may be x.                          */
+typedef enum {
+  QMOE_FORM_BF16 = 0,
+  QMOE_FORM_F32 = 1,
+  QMOE_FORM_INT8 = 2,
+  QMOE_FORM_E4M3 = 3,
+  QMOE_FORM_E4M3_B128 = 4
+} qmoe_form;
+typedef enum {
+  QMOE_GATE_NONE = 0,
+  QMOE_GATE_COLUMN = 1,
+  QMOE_GATE_TOKEN = 2,
+  QMOE_GATE_FULL = 3
+} qmoe_gate;
+qmoe_status qmoe_pre_norm(const void* x, int32_t dtype, const float* w, float eps, int32_t T,
+                          int32_t H, int32_t form, void* n, float* scale, void* stream);
+qmoe_status qmoe_post_norm(const void* y, const void* x, int32_t dtype, const float* w,
+                           const void* gate, int32_t gate_kind, float alpha, float eps, int32_t T,
+                           int32_t H, void* out, const float* next_w, int32_t form, void* n,
+                           float* scale, void* stream);
+/* Gradients.  Nothing of the forward pass but its inputs is needed.
+ * qmoe_pre_norm_backward -- dn the gradient of n: dx = the norm's input
+ *   gradient + dres (optional: the gradient that reaches x along the
+ *   residual stream; dx may be dres), dw fp32 [H].
+ * qmoe_post_norm_backward -- dout the gradient of out: dy, dres =
+ *   alpha * dout (x's gradient), dw fp32 [H], dgate in the gate's shape and
+ *   type (NULL without a gate).
+ * dw and a column gate's dgate are sums over the tokens in a fixed order
+ * (T = 0 gives zeros).  ws: qmoe_norm_backward_workspace(H) bytes, 256-byte
+ * aligned, contents need no initialisation; calls that share it must be
+ * ordered on one stream.                                                 */
+size_t qmoe_norm_backward_workspace(int32_t H);
+qmoe_status qmoe_pre_norm_backward(const void* dn, const void* x, int32_t dtype, const float* w,
+                                   float eps, const void* dres, int32_t T, int32_t H, void* dx,
+                                   float* dw, void* ws, size_t ws_bytes, void* stream);
+qmoe_status qmoe_post_norm_backward(const void* dout, const void* y, int32_t dtype,
+                                    const float* w, const void* gate, int32_t gate_kind,
+                                    float alpha, float eps, int32_t T, int32_t H, void* dy,
+                                    void* dres, float* dw, void* dgate, void* ws, size_t ws_bytes,
+                                    void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,13 +11,14 @@
 #include <string>
 
 #include "qmoe.h"
+#include "block_internal.h"
 #include "qmoe_internal.h"
 
 namespace qmoe {
 
 static thread_local int g_last_hip_error = 0;
 
-static qmoe_status hip_status(hipError_t e) {
+qmoe_status hip_status(hipError_t e) {
   if (e == hipSuccess) return QMOE_OK;
   g_last_hip_error = (int)e;
   return QMOE_ERR_HIP;

@@ -31,8 +31,13 @@ EXPORTS = (
     "qmoe_align_noalloc", "qmoe_route_align", "qmoe_default_block_m",
     "qmoe_grouped_ffn_workspace", "qmoe_grouped_ffn_debug_offsets", "qmoe_grouped_ffn",
     "qmoe_grouped_ffn_profiled", "qmoe_combine", "qmoe_prepack", "qmoe_decode_workspace",
-    "qmoe_decode",
+    "qmoe_decode", "qmoe_fp8_quant", "qmoe_fp8_matmul_workspace", "qmoe_fp8_matmul",
+    "qmoe_fp8_grouped_matmul", "qmoe_balance_workspace", "qmoe_balance", "qmoe_balance_backward",
+    "qmoe_pre_norm", "qmoe_post_norm", "qmoe_norm_backward_workspace", "qmoe_pre_norm_backward",
+    "qmoe_post_norm_backward",
 )
+# Forms in which pre_norm and post_norm write a norm (qmoe_form).
+NORM_FORMS = {"bf16": 0, "f32": 1, "int8": 2, "e4m3": 3, "e4m3_128": 4}
 # Largest batch qmoe_decode takes (QMOE_DECODE_MAX_TOKENS).
 DECODE_MAX_TOKENS = 16
 # Batches up to this size take the one-launch qmoe_decode in moe_forward's
@@ -118,6 +123,25 @@ def _lib() -> ctypes.CDLL:
     L.qmoe_decode.restype = ctypes.c_int
     L.qmoe_decode.argtypes = [ctypes.POINTER(FfnDesc), vp, vp, vp, ctypes.POINTER(Weights), vp,
                               vp, vp, vp, vp, vp, sz, vp]
+    f32 = ctypes.c_float
+    for name, res, args in (
+            ("qmoe_fp8_quant", ctypes.c_int, [vp] + [i32] * 6 + [vp] * 5),
+            ("qmoe_fp8_matmul_workspace", sz, [i32] * 3),
+            ("qmoe_fp8_matmul", ctypes.c_int, [vp] * 4 + [i32] * 4 + [vp, i32, vp, sz, vp]),
+            ("qmoe_fp8_grouped_matmul", ctypes.c_int,
+             [vp, vp, i32] + [vp] * 5 + [i32] * 6 + [vp, i32, vp]),
+            ("qmoe_balance_workspace", sz, [i32] * 2),
+            ("qmoe_balance", ctypes.c_int, [vp] * 3 + [i32] * 3 + [f32] + [vp] * 5 + [sz, vp]),
+            ("qmoe_balance_backward", ctypes.c_int, [vp] * 5 + [i32] * 3 + [f32, vp, vp]),
+            ("qmoe_pre_norm", ctypes.c_int, [vp, i32, vp, f32] + [i32] * 3 + [vp] * 3),
+            ("qmoe_post_norm", ctypes.c_int,
+             [vp, vp, i32, vp, vp, i32, f32, f32, i32, i32, vp, vp, i32, vp, vp, vp]),
+            ("qmoe_norm_backward_workspace", sz, [i32]),
+            ("qmoe_pre_norm_backward", ctypes.c_int,
+             [vp, vp, i32, vp, f32, vp, i32, i32, vp, vp, vp, sz, vp]),
+            ("qmoe_post_norm_backward", ctypes.c_int,
+             [vp, vp, i32, vp, vp, i32, f32, f32, i32, i32, vp, vp, vp, vp, vp, sz, vp])):
+        getattr(L, name).restype, getattr(L, name).argtypes = res, args
     _LIB = L
     return L
 
@@ -438,3 +462,351 @@ def decode_forward(scheme: str, logits: torch.Tensor, x: torch.Tensor,
     return {"topk_ids": ids, "topk_w": w, "y_pairs": y_pairs, "ws": ws, "out": ob,
             "out_f32": of if want_f32 else None}
 
+
+
+# ---------------------------------------------------------------- around the experts
+# Block-128 fp8 quantizer and products, balance loss, norms.  These check
+# shapes, types and devices here (ValueError), since the C ABI sees pointers
+# only, and run on the current stream of the tensors' device.
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _tensor(t, name: str, shape, *dtypes):
+    _need(isinstance(t, torch.Tensor), f"{name} must be a tensor")
+    _need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not "
+                                          f"{tuple(t.shape)}")
+    _need(t.dtype in dtypes, f"{name} must be {' or '.join(str(d) for d in dtypes)}, not "
+                             f"{t.dtype}")
+
+
+def _one_device(*ts):
+    """The device of the tensors given (None for one left out)."""
+    devs = {t.device for t in ts if t is not None}
+    _need(len(devs) == 1 and next(iter(devs)).type == "cuda",
+          f"all tensors must live on one GPU, not on {sorted(map(str, devs))}")
+    return next(iter(devs))
+
+
+def _call(dev, name: str, *args):
+    """The library call `name` with the device current (a launch goes to the
+    current device's context) and its current stream as the last argument."""
+    with torch.cuda.device(dev):
+        _check(getattr(_lib(), name)(*args, _stream(dev)), name)
+
+
+def _float_kind(t, name: str) -> int:
+    _need(t.dtype in (torch.bfloat16, torch.float32), f"{name} must be bfloat16 or float32, not "
+                                                      f"{t.dtype}")
+    return QMOE_DT_F32 if t.dtype == torch.float32 else QMOE_DT_BF16
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def fp8_quant(x: torch.Tensor, block: bool = False, act: Optional[str] = None, rows: bool = True,
+              cols: bool = False) -> dict:
+    """qmoe_fp8_quant.  x [M, K] (weights with block=True: [N, K] or the stack
+    [E, N, K]; act="silu_mul": [M, 2K] = gate | up).  Returns "codes" (uint8
+    e4m3) and "scale" with `rows`, "codes_t" and "scale_t" (the transpose,
+    groups along the columns of x) with `cols`."""
+    _need(act in (None, "silu_mul"), f"act must be None or 'silu_mul', not {act!r}")
+    _need(rows or cols, "rows or cols (or both)")
+    _need(not (block and act), "block scales are for weights: act does not go with them")
+    _need(x.dim() == 2 or (block and x.dim() == 3), "x must be [M, K] (or [E, N, K] with block)")
+    dt, dev = _float_kind(x, "x"), _one_device(x)
+    B = x.shape[0] if x.dim() == 3 else 1
+    M, K = x.shape[-2:]
+    if act:
+        _need(K % 2 == 0, "act='silu_mul' takes [M, 2K]")
+        K //= 2
+    _need(K >= 1, "x has no columns")
+    lead = (B,) if x.dim() == 3 else ()
+    out = {}
+
+    def new(shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+    if rows:
+        out["codes"] = new(lead + (M, 128 * _blocks(K)), torch.uint8)
+        out["scale"] = new(lead + ((_blocks(M), _blocks(K)) if block else (_blocks(K), M)),
+                           torch.float32)
+    if cols:
+        out["codes_t"] = new(lead + (K, 128 * _blocks(M)), torch.uint8)
+        out["scale_t"] = new(lead + ((_blocks(K), _blocks(M)) if block else (_blocks(M), K)),
+                             torch.float32)
+    _call(dev, "qmoe_fp8_quant", _ptr(x), dt, B, M, K, int(block), int(act is not None),
+          _ptr(out.get("codes")), _ptr(out.get("scale")), _ptr(out.get("codes_t")),
+          _ptr(out.get("scale_t")))
+    return out
+
+
+def _operand(codes, scale, name: str, block: bool, lead=()):
+    """Checks codes [.., rows, K] with their scales; returns (rows, K)."""
+    _need(codes.dim() == 2 + len(lead), f"{name} must have {2 + len(lead)} axes")
+    n, k = codes.shape[-2:]
+    _need(k >= 128 and k % 128 == 0, f"{name}'s row length {k} is not a multiple of 128")
+    _tensor(codes, name, lead + (n, k), torch.uint8)
+    _tensor(scale, f"{name}_scale", lead + ((_blocks(n), k // 128) if block else (k // 128, n)),
+            torch.float32)
+    return n, k
+
+
+def _out(out, shape, dtype, dev):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _tensor(out, "out", shape, dtype)
+    return out
+
+
+def fp8_matmul_workspace(M: int, N: int, K: int) -> int:
+    return int(_lib().qmoe_fp8_matmul_workspace(M, N, K))
+
+
+def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+               b_block: bool = True, out_dtype: torch.dtype = torch.bfloat16,
+               ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
+    """qmoe_fp8_matmul: a [M, K] . b [N, K]^T -> [M, N] of e4m3 codes (uint8);
+    b_block says that b's scales are per 128 x 128 block, not per row."""
+    M, K = _operand(a, a_scale, "a", False)
+    N, K2 = _operand(b, b_scale, "b", b_block)
+    _need(K == K2, f"a's rows have {K} values, b's {K2}")
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    dev = _one_device(a, a_scale, b, b_scale, ws, out)
+    out = _out(out, (M, N), out_dtype, dev)
+    need = fp8_matmul_workspace(M, N, K)
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = _ws(need, dev) if need else None
+    _call(dev, "qmoe_fp8_matmul", _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), int(b_block), M,
+          N, K, _ptr(out), _float_kind(out, "out"), _ptr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return out
+
+
+def fp8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
+                       b_scale: torch.Tensor, al: dict, k: int, pair_rows: bool = False,
+                       out_dtype: torch.dtype = torch.bfloat16,
+                       out: Optional[torch.Tensor] = None):
+    """qmoe_fp8_grouped_matmul: row p of the result is a[row(p)] . b[expert of
+    pair p]^T, row(p) = p // k (a [T, K]) or p (pair_rows, a [T*k, K]);
+    `al` is align's (or route_align's) result."""
+    _need(b.dim() == 3, "b must be [E, N, K]")
+    E = b.shape[0]
+    rows, K = _operand(a, a_scale, "a", False)
+    N, K2 = _operand(b, b_scale, "b", True, (E,))
+    _need(K == K2, f"a's rows have {K} values, b's {K2}")
+    _need(k >= 1 and (not pair_rows or rows % k == 0), f"{rows} pair rows are not a multiple of "
+                                                        f"k = {k}")
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    T, bm = rows // k if pair_rows else rows, al["block_m"]
+    cap = align_capacity(T, k, E, bm)
+    _need(cap > 0, f"bad sizes: T {T}, k {k}, E {E}, block_m {bm}")
+    _tensor(al["sorted_pair_ids"], "sorted_pair_ids", (cap,), torch.int32)
+    _tensor(al["tile_expert"], "tile_expert", (cap // bm,), torch.int32)
+    _tensor(al["num_padded"], "num_padded", (1,), torch.int32)
+    dev = _one_device(a, a_scale, b, b_scale, al["sorted_pair_ids"], al["tile_expert"],
+                      al["num_padded"], out)
+    out = _out(out, (T * k, N), out_dtype, dev)
+    _call(dev, "qmoe_fp8_grouped_matmul", _ptr(a), _ptr(a_scale), int(pair_rows), _ptr(b),
+          _ptr(b_scale), _ptr(al["sorted_pair_ids"]), _ptr(al["tile_expert"]),
+          _ptr(al["num_padded"]), T, k, E, bm, N, K, _ptr(out), _float_kind(out, "out"))
+    return out
+
+
+def fp8_block_m(T: int, k: int, E: int) -> int:
+    """Tile height (align's block_m) for the block-128 fp8 expert products:
+    the smallest that holds the mean rows per expert."""
+    mean = T * k / E
+    return 16 if mean <= 16 else 32 if mean <= 32 else 64 if mean <= 64 else 128
+
+
+def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor, weights: dict,
+                    k: int) -> dict:
+    """The layer with block-128 fp8 experts: route -> align -> gate/up product
+    -> SiLU*mul and quantization -> down product -> combine.  x [T, H] codes
+    with x_scale [H/128, T] (fp8_quant or a norm's "e4m3_128" form); weights:
+    w13 [E, 2I, H], w2 [E, H, I] codes and their 128 x 128 block scales
+    (fp8_quant(w, block=True)), H % 128 == 0, I % 128 == 0."""
+    T, E = logits.shape
+    _need(x.shape[0] == T, f"x has {x.shape[0]} rows, logits {T}")
+    block_m = fp8_block_m(T, k, E)
+    with torch.cuda.device(_one_device(logits, x)):
+        ids, w, al = route_align(logits, k, block_m)
+        gu = fp8_grouped_matmul(x, x_scale, weights["w13"], weights["w13_scale"], al, k)
+        h = fp8_quant(gu, act="silu_mul")
+        y = fp8_grouped_matmul(h["codes"], h["scale"], weights["w2"], weights["w2_scale"], al, k,
+                               pair_rows=True)
+        out, _ = combine(y, w)
+    return {"topk_ids": ids, "topk_w": w, "align": al, "y_pairs": y, "out": out}
+
+
+def _mask_ptr(mask, T: int):
+    if mask is None:
+        return None
+    _tensor(mask, "mask", (T,), torch.uint8, torch.bool)
+    return _ptr(mask)
+
+
+def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
+                 mask: Optional[torch.Tensor] = None, coef: float = 1.0,
+                 ws: Optional[torch.Tensor] = None) -> dict:
+    """qmoe_balance: {"loss" fp32 [1], "counts" int32 [E], "probs" fp32 [E],
+    "tokens" int32 [1]} of router logits [T, E] and their picks [T, k]; mask
+    [T] (uint8 or bool): 0 drops a token."""
+    _need(logits.dim() == 2 and topk_ids.dim() == 2, "logits must be [T, E] and topk_ids [T, k]")
+    T, E = logits.shape
+    k = topk_ids.shape[1]
+    _tensor(logits, "logits", (T, E), torch.float32)
+    _tensor(topk_ids, "topk_ids", (T, k), torch.int32)
+    dev = _one_device(logits, topk_ids, mask, ws)
+    need = int(_lib().qmoe_balance_workspace(T, E))
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = _ws(need, dev)
+    r = {"loss": torch.empty(1, dtype=torch.float32, device=dev),
+         "counts": torch.empty(E, dtype=torch.int32, device=dev),
+         "probs": torch.empty(E, dtype=torch.float32, device=dev),
+         "tokens": torch.empty(1, dtype=torch.int32, device=dev)}
+    _call(dev, "qmoe_balance", _ptr(logits), _ptr(topk_ids), _mask_ptr(mask, T), T, E, k, coef,
+          _ptr(r["loss"]), _ptr(r["counts"]), _ptr(r["probs"]), _ptr(r["tokens"]), _ptr(ws),
+          ws.numel() * ws.element_size())
+    return r
+
+
+def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor,
+                          k: int, dloss: torch.Tensor, mask: Optional[torch.Tensor] = None,
+                          coef: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qmoe_balance_backward: the gradient of balance_loss (same logits, mask
+    and coef, its counts and tokens) to the logits; dloss fp32 [1]."""
+    _need(logits.dim() == 2, "logits must be [T, E]")
+    T, E = logits.shape
+    _tensor(logits, "logits", (T, E), torch.float32)
+    _tensor(counts, "counts", (E,), torch.int32)
+    _tensor(tokens, "tokens", (1,), torch.int32)
+    _tensor(dloss, "dloss", (1,), torch.float32)
+    dev = _one_device(logits, counts, tokens, dloss, mask, out)
+    out = _out(out, (T, E), torch.float32, dev)
+    _call(dev, "qmoe_balance_backward", _ptr(logits), _mask_ptr(mask, T), _ptr(counts),
+          _ptr(tokens), _ptr(dloss), T, E, k, coef, _ptr(out))
+    return out
+
+
+def _new_form(form: str, T: int, H: int, dev):
+    """Code of a form and its new (n, scale)."""
+    _need(form in NORM_FORMS, f"a norm is written as one of {sorted(NORM_FORMS)}, not {form!r}")
+    if form in ("bf16", "f32"):
+        dt = torch.bfloat16 if form == "bf16" else torch.float32
+        return NORM_FORMS[form], torch.empty((T, H), dtype=dt, device=dev), None
+    if form == "e4m3_128":
+        n = torch.empty((T, 128 * _blocks(H)), dtype=torch.uint8, device=dev)
+        return NORM_FORMS[form], n, torch.empty((_blocks(H), T), dtype=torch.float32, device=dev)
+    n = torch.empty((T, H), dtype=torch.int8 if form == "int8" else torch.uint8, device=dev)
+    return NORM_FORMS[form], n, torch.empty(T, dtype=torch.float32, device=dev)
+
+
+def _gate_kind(gate, T: int, H: int, dtype):
+    """(qmoe_gate, its pointer) of a gate that broadcasts to [T, H] as torch
+    tensors do: None, fp32 [H] per column, fp32 [T, 1] per token, or [T, H] in
+    the activations' type."""
+    if gate is None:
+        return 0, None
+    if gate.dim() == 1:
+        _tensor(gate, "a gate per column", (H,), torch.float32)
+        return 1, _ptr(gate)
+    if tuple(gate.shape) == (T, 1) and (H > 1 or gate.dtype != dtype):
+        _tensor(gate, "a gate per token", (T, 1), torch.float32)
+        return 2, _ptr(gate)
+    _tensor(gate, "gate", (T, H), dtype)
+    return 3, _ptr(gate)
+
+
+def pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, out: str = "bf16"):
+    """qmoe_pre_norm: (n, scale) with n = x / rms(x) * weight in the form
+    `out`: "bf16", "f32" (scale None), "int8" or "e4m3" (scale [T]: the
+    grouped FFN's x and x_scale), "e4m3_128" (scale [H/128, T])."""
+    _need(x.dim() == 2, "x must be [T, H]")
+    T, H = x.shape
+    dt = _float_kind(x, "x")
+    _tensor(weight, "weight", (H,), torch.float32)
+    dev = _one_device(x, weight)
+    form, n, scale = _new_form(out, T, H, dev)
+    _call(dev, "qmoe_pre_norm", _ptr(x), dt, _ptr(weight), eps, T, H, form, _ptr(n), _ptr(scale))
+    return n, scale
+
+
+def post_norm(y: torch.Tensor, weight: torch.Tensor, x: torch.Tensor,
+              gate: Optional[torch.Tensor] = None, alpha: float = 1.0, eps: float = 1e-6,
+              next_weight: Optional[torch.Tensor] = None, next_out: str = "bf16",
+              out: Optional[torch.Tensor] = None):
+    """qmoe_post_norm: (out, n, scale) with out = alpha * x + gate * (y /
+    rms(y) * weight) and, with next_weight, the next block's norm of out in
+    the form next_out (as pre_norm gives; else n and scale are None).
+    ``out`` may be x."""
+    _need(y.dim() == 2, "y must be [T, H]")
+    T, H = y.shape
+    dt = _float_kind(y, "y")
+    _tensor(x, "x", (T, H), y.dtype)
+    _tensor(weight, "weight", (H,), torch.float32)
+    dev = _one_device(y, x, weight, gate, next_weight, out)
+    kind, gp = _gate_kind(gate, T, H, y.dtype)
+    out = _out(out, (T, H), y.dtype, dev)
+    form, n, scale = 0, None, None
+    if next_weight is not None:
+        _tensor(next_weight, "next_weight", (H,), torch.float32)
+        form, n, scale = _new_form(next_out, T, H, dev)
+    _call(dev, "qmoe_post_norm", _ptr(y), _ptr(x), dt, _ptr(weight), gp, kind, alpha, eps, T, H,
+          _ptr(out), _ptr(next_weight), form, _ptr(n), _ptr(scale))
+    return out, n, scale
+
+
+def _norm_ws(ws, H: int, dev):
+    need = int(_lib().qmoe_norm_backward_workspace(H))
+    if ws is None or ws.numel() * ws.element_size() < need:
+        ws = _ws(need, dev)
+    return ws, ws.numel() * ws.element_size()
+
+
+def pre_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                      dres: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """qmoe_pre_norm_backward: (dx, dweight) for the gradient dn of pre_norm's
+    n; dres, the gradient that reaches x along the residual stream, is added
+    to dx."""
+    _need(x.dim() == 2, "x must be [T, H]")
+    T, H = x.shape
+    dt = _float_kind(x, "x")
+    _tensor(dn, "dn", (T, H), x.dtype)
+    _tensor(weight, "weight", (H,), torch.float32)
+    if dres is not None:
+        _tensor(dres, "dres", (T, H), x.dtype)
+    dev = _one_device(dn, x, weight, dres, ws)
+    dx = torch.empty_like(x)
+    dw = torch.empty(H, dtype=torch.float32, device=dev)
+    ws, nbytes = _norm_ws(ws, H, dev)
+    _call(dev, "qmoe_pre_norm_backward", _ptr(dn), _ptr(x), dt, _ptr(weight), eps, _ptr(dres), T,
+          H, _ptr(dx), _ptr(dw), _ptr(ws), nbytes)
+    return dx, dw
+
+
+def post_norm_backward(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor,
+                       gate: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                       eps: float = 1e-6, ws: Optional[torch.Tensor] = None) -> dict:
+    """qmoe_post_norm_backward: {"dy", "dres" (x's gradient, alpha * dout),
+    "dw", "dgate" (None without a gate)} for the gradient dout of post_norm's
+    out."""
+    _need(y.dim() == 2, "y must be [T, H]")
+    T, H = y.shape
+    dt = _float_kind(y, "y")
+    _tensor(dout, "dout", (T, H), y.dtype)
+    _tensor(weight, "weight", (H,), torch.float32)
+    dev = _one_device(dout, y, weight, gate, ws)
+    kind, gp = _gate_kind(gate, T, H, y.dtype)
+    r = {"dy": torch.empty_like(y), "dres": torch.empty_like(y),
+         "dw": torch.empty(H, dtype=torch.float32, device=dev),
+         "dgate": None if gate is None else torch.empty_like(gate)}
+    ws, nbytes = _norm_ws(ws, H, dev)
+    _call(dev, "qmoe_post_norm_backward", _ptr(dout), _ptr(y), dt, _ptr(weight), gp, kind, alpha,
+          eps, T, H, _ptr(r["dy"]), _ptr(r["dres"]), _ptr(r["dw"]), _ptr(r["dgate"]), _ptr(ws),
+          nbytes)
+    return r

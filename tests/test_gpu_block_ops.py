@@ -1,0 +1,450 @@
+"""The fp8 quantizer and products and the balance loss against their 64-bit
+forms, at the sizes and values where they can go wrong."""
+import pytest
+import torch
+
+import _block_ref as R
+from quantized_mixture_experts_moe_amd import ops
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _rand(*shape, seed=0, scale=1.0, dtype=F32):
+    g = torch.Generator("cuda")
+    g.manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(dtype)
+
+
+def _offset(t, n=1):
+    """A contiguous copy of t whose address is n elements past an aligned one."""
+    buf = torch.empty(t.numel() + 16, dtype=t.dtype, device=t.device)
+    v = buf[n:n + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+# ---------------------------------------------------------------- quantizer
+
+def _check_groups(codes, scale, v, dim, err=0.0):
+    """codes [M, up128(K)] with scale [K/128, M] against values v [M, K] in 64
+    bits (dim 1), or codes_t / scale_t (dim 0).  err: relative error of the
+    values the kernel quantizes (0: v is exact, then the codes are the nearest
+    e4m3 values of the correctly rounded quotients)."""
+    if dim == 0:
+        v = v.t()
+    M, K = v.shape
+    Kp = R.up128(K)
+    assert codes.shape == (M, Kp) and scale.shape == (Kp // 128, M)
+    assert not codes[:, K:].any()
+    g = R.pad_to(v, Kp, 1).reshape(M, Kp // 128, 128)
+    s = R.group_scale(g.abs().amax(2))
+    got = scale.t().double()
+    assert torch.equal(got.isnan(), s.isnan())
+    fine = ~s.isnan()
+    # amax / 448: one rounding, and the values' own error
+    assert ((got - s).abs()[fine] <= s[fine] * (R.U32 + err)).all()
+    q = R.codes_value(codes).view(M, Kp // 128, 128)
+    assert not q[~fine].any()
+    if err == 0.0:
+        # the quotient in fp32 of the scale as stored, correctly rounded
+        want = R.e4m3((g.float() / got.float().unsqueeze(2)).double())
+        assert torch.equal(q[fine], want[fine])
+    else:
+        # half a step of e4m3: 2^-4 relative, 2^-10 below the normal range;
+        # the quotient and the values are off by a few fp32 roundings
+        t = g[fine] / got[fine].unsqueeze(1)
+        tol = (t.abs() * 2.0 ** -4).clamp(min=2.0 ** -10) + t.abs() * (err + 2 * R.U32)
+        assert ((q[fine] - t).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 128), (3, 127), (17, 129), (128, 128), (130, 256),
+                                 (257, 40), (1000, 777), (64, 2048), (5, 4100), (1, 16384)])
+def test_quant_rows_and_columns(M, K, dtype):
+    x = _rand(M, K, seed=M + K, dtype=dtype)
+    x[M // 2] = 0
+    x[:, K // 2] *= 300
+    v = x.double()
+    for rows, cols in ((True, False), (False, True), (True, True)):
+        r = ops.fp8_quant(x, rows=rows, cols=cols)
+        assert set(r) == ({"codes", "scale"} if rows else set()) | (
+            {"codes_t", "scale_t"} if cols else set())
+        if rows:
+            _check_groups(r["codes"], r["scale"], v, 1)
+        if cols:
+            _check_groups(r["codes_t"], r["scale_t"], v, 0)
+    r = ops.fp8_quant(_offset(x), cols=True)  # no 16-byte loads
+    _check_groups(r["codes"], r["scale"], v, 1)
+    _check_groups(r["codes_t"], r["scale_t"], v, 0)
+    r = ops.fp8_quant(_offset(x))
+    _check_groups(r["codes"], r["scale"], v, 1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_quant_corner_values(dtype):
+    x = _rand(140, 512, seed=5, dtype=dtype)
+    x[0, 3] = float("nan")
+    x[1, 200] = float("inf")
+    x[2, 300] = -float("inf")
+    x[3] = 1e-39          # below the normal range: the scale stops at 2^-126
+    x[4] = 0
+    x[4, 130] = -1e-39
+    x[5] = 3e38
+    x[6, ::2] = -0.0
+    r = ops.fp8_quant(x, cols=True)
+    _check_groups(r["codes"], r["scale"], x.double(), 1)
+    _check_groups(r["codes_t"], r["scale_t"], x.double(), 0)
+    r = ops.fp8_quant(x)
+    _check_groups(r["codes"], r["scale"], x.double(), 1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,K", [(1, 64), (5, 129), (300, 768), (33, 1001)])
+def test_quant_silu_mul(M, K, dtype):
+    x = _rand(M, 2 * K, seed=M * K, scale=3.0, dtype=dtype)
+    x[0, 0] = -200.0  # exp overflows: SiLU is -0
+    x[0, K - 1] = 200.0
+    h = R.silu_mul(x).float().double()  # as fp32 holds it: SiLU(-200) is below its range
+    # exp to 2 ulp, the sum, the division and the product: 2^-24 * (4 + 3);
+    # the exponential's own error shrinks in 1 + exp
+    err = 8 * R.U32
+    for cols in (False, True):
+        r = ops.fp8_quant(x, act="silu_mul", cols=cols)
+        _check_groups(r["codes"], r["scale"], h, 1, err)
+        if cols:
+            _check_groups(r["codes_t"], r["scale_t"], h, 0, err)
+
+
+@pytest.mark.parametrize("shape", [(128, 128), (1, 1), (200, 300), (3, 130, 256), (2, 64, 129)])
+def test_quant_blocks(shape):
+    w = _rand(*shape, seed=sum(shape), dtype=BF)
+    r = ops.fp8_quant(w, block=True, cols=True)
+    lead, (N, K) = shape[:-2], shape[-2:]
+    Np, Kp = R.up128(N), R.up128(K)
+    assert r["codes"].shape == lead + (N, Kp) and r["codes_t"].shape == lead + (K, Np)
+    assert r["scale"].shape == lead + (Np // 128, Kp // 128)
+    assert r["scale_t"].shape == lead + (Kp // 128, Np // 128)
+    v = R.pad_to(R.pad_to(w.double().reshape(-1, N, K), Np, 1), Kp, 2)
+    B = v.shape[0]
+    t = v.view(B, Np // 128, 128, Kp // 128, 128)
+    amax = t.abs().amax((2, 4))
+    s = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax)).float()  # one rounding
+    assert torch.equal(r["scale"].view(s.shape), s)
+    assert torch.equal(r["scale_t"].view(B, Kp // 128, Np // 128), s.transpose(1, 2))
+    want = R.e4m3((t.float() / s[:, :, None, :, None]).double()).view(B, Np, Kp)
+    assert torch.equal(R.codes_value(r["codes"]).view(B, N, Kp), want[:, :N])
+    assert torch.equal(R.codes_value(r["codes_t"]).view(B, K, Np),
+                       want[:, :, :K].transpose(1, 2))
+    assert torch.equal(ops.fp8_quant(w, block=True)["codes"], r["codes"])
+    only_t = ops.fp8_quant(w, block=True, rows=False, cols=True)
+    assert torch.equal(only_t["codes_t"], r["codes_t"])
+
+
+def test_quant_empty():
+    r = ops.fp8_quant(torch.empty(0, 256, device="cuda"), cols=True)
+    assert r["codes"].shape == (0, 256) and r["codes_t"].shape == (256, 0)
+
+
+# ---------------------------------------------------------------- products
+
+def _operands(M, N, K, b_block, seed=0):
+    a = ops.fp8_quant(_rand(M, K, seed=seed, scale=2.0))
+    w = _rand(N, K, seed=seed + 1, scale=K ** -0.5)
+    b = ops.fp8_quant(w, block=b_block)
+    return a["codes"], a["scale"], b["codes"], b["scale"]
+
+
+def _close(out, a, b, K):
+    """out against the 64-bit product of the operands' values.  fp32: a K
+    block's 128 products are exact and summed in fp32, each step off by at most
+    one place (two half steps) of the running sum of magnitudes; then two scale
+    roundings and one addition per K block (and per part of a split).  bf16:
+    besides, the fp8 matrix instruction lines products up in eights with the
+    largest of the eight; one 12 bits below it is kept whole and one 14 bits
+    below is lost, so each is off by at most 2^-12 of the largest, and the
+    eight by 2^-9 of it, which is at most 2^-9 of their magnitudes' sum."""
+    ref, mag = a @ b.t(), a.abs() @ b.abs().t()
+    lined_up = 2.0 ** -9 if out.dtype == BF else 0.0
+    tol = R.half_step(out.dtype) * ref.abs() + \
+        ((2 * 128 + 4 + 2 * (K // 128)) * R.U32 + lined_up) * mag + 1e-38
+    bad = (out.double() - ref).abs() > tol
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off, first at " \
+                          f"{bad.nonzero()[0].tolist()}"
+    if out.dtype == BF and ref.numel() >= 256:
+        # the 2-norm: 2^-8 / sqrt(3) at most from the output's rounding
+        assert float((out.double() - ref).norm() / ref.norm()) <= 2.0 ** -8 / 3 ** 0.5 * 1.05
+
+
+MATMUL = [(1, 1, 128), (1, 2048, 2048), (2, 130, 256), (5, 63, 384), (15, 16, 128), (16, 64, 512),
+          (17, 513, 640), (31, 33, 128), (33, 255, 256), (48, 1000, 384), (64, 256, 1024),
+          (65, 129, 2304), (100, 384, 4096), (128, 128, 128), (129, 257, 384), (200, 200, 2048),
+          (256, 256, 256), (300, 500, 640), (511, 777, 512), (640, 1024, 256), (1000, 129, 4224),
+          (2048, 300, 128), (2000, 2100, 384), (4100, 512, 256), (3, 8192, 128), (8, 16, 8192)]
+
+
+@pytest.mark.parametrize("b_block", [True, False])
+@pytest.mark.parametrize("M,N,K", MATMUL)
+def test_matmul(M, N, K, b_block):
+    print(f"matmul {M} {N} {K} {b_block}", flush=True)
+    a, sa, b, sb = _operands(M, N, K, b_block, seed=M + N)
+    av, bv = R.wide(a, sa), R.wide(b, sb, b_block)
+    for dt in (BF, F32):
+        out = torch.full((M, N), float("nan"), dtype=dt, device="cuda")
+        got = ops.fp8_matmul(a, sa, b, sb, b_block=b_block, out_dtype=dt, out=out)
+        assert got is out
+        _close(out, av, bv, K)
+        again = ops.fp8_matmul(a, sa, b, sb, b_block=b_block, out_dtype=dt)
+        assert torch.equal(again, out)  # the same bits every time
+
+
+@pytest.mark.parametrize("M", [1, 40, 200, 600])
+def test_matmul_leaves_what_is_around_out(M):
+    N, K = 131, 384
+    a, sa, b, sb = _operands(M, N, K, True)
+    buf = torch.full((M * N + 64,), 7.0, dtype=BF, device="cuda")
+    for off in (0, 1, 8, 13):
+        buf.fill_(7.0)
+        out = buf[off:off + M * N].view(M, N)
+        ops.fp8_matmul(a, sa, b, sb, out=out)
+        _close(out, R.wide(a, sa), R.wide(b, sb, True), K)
+        assert (buf[:off] == 7).all() and (buf[off + M * N:] == 7).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 96, 256), (40, 130, 512), (300, 300, 384), (520, 640, 256)])
+def test_matmul_is_exact_on_small_whole_numbers(M, N, K):
+    g = torch.Generator("cuda")
+    g.manual_seed(M)
+    a = torch.randint(-8, 9, (M, K), generator=g, device="cuda").float()
+    b = torch.randint(-8, 9, (N, K), generator=g, device="cuda").float()
+    code = lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8)  # noqa: E731
+    sa = torch.exp2(torch.randint(-3, 4, (K // 128, M), generator=g, device="cuda").float())
+    for b_block, shape in ((True, ((N + 127) // 128, K // 128)), (False, (K // 128, N))):
+        sb = torch.exp2(torch.randint(-3, 4, shape, generator=g, device="cuda").float())
+        ac, bc = code(a), code(b)
+        out = ops.fp8_matmul(ac, sa, bc, sb, b_block=b_block, out_dtype=F32)
+        assert torch.equal(out.double(), R.wide(ac, sa) @ R.wide(bc, sb, b_block).t())
+
+
+@pytest.mark.parametrize("M", [1, 20, 70, 300])
+def test_matmul_not_finite_stays_in_its_row_and_column(M):
+    N, K = 200, 512
+    x, w = _rand(M, K, seed=1), _rand(N, K, seed=2)
+    x[0, 5] = float("inf")
+    w[3, 400] = float("nan")
+    a, b = ops.fp8_quant(x), ops.fp8_quant(w)
+    out = ops.fp8_matmul(a["codes"], a["scale"], b["codes"], b["scale"], b_block=False)
+    bad = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    bad[0] = True
+    bad[:, 3] = True
+    assert torch.equal(out.isnan(), bad)
+
+
+def test_linear_layer_gradients():
+    """dx and dw through the quantizer's transposes against differences of the
+    64-bit linear loss sum(dy * (x w^T)): exact up to the quantization, which
+    moves a value by at most 2^-4 of itself (or 2^-10 of its group's scale)."""
+    T, N, K = 300, 200, 256
+    x, w, dy = _rand(T, K, seed=1), _rand(N, K, seed=2), _rand(T, N, seed=3)
+    qw = ops.fp8_quant(w, block=True, cols=True)
+    qx, qy = ops.fp8_quant(x, cols=True), ops.fp8_quant(dy, cols=True)
+    dx = ops.fp8_matmul(qy["codes"], qy["scale"], qw["codes_t"], qw["scale_t"], out_dtype=F32)
+    dw = ops.fp8_matmul(qy["codes_t"], qy["scale_t"], qx["codes_t"], qx["scale_t"], b_block=False,
+                        out_dtype=F32)
+    assert dx.shape == (T, R.up128(K)) and dw.shape == (N, K)
+    # the formula on the quantized values
+    _close(dx, R.wide(qy["codes"], qy["scale"]), R.wide(qw["codes_t"], qw["scale_t"], True), 256)
+    _close(dw, R.wide(qy["codes_t"], qy["scale_t"]), R.wide(qx["codes_t"], qx["scale_t"]),
+           R.up128(T))
+
+    # differences of the loss along the gradient's own direction
+    def loss(xx, ww):
+        return (dy.double() * (xx @ ww.t())).sum()
+    x64, w64 = x.double(), w.double()
+
+    def slack(p, q, ps, qs):  # sum of |error| of a product of quantized factors
+        ep, eq = p.abs() * 2.0 ** -4 + ps, q.abs() * 2.0 ** -4 + qs
+        return ep @ q.abs() + (p.abs() + ep) @ eq
+    low = 2.0 ** -10
+    top = lambda t: float(t.abs().max()) / 448 * low  # noqa: E731
+    for grad, along, base, tol in (
+            (dx, lambda h, d: loss(x64 + h * d, w64), x64,
+             slack(dy.double(), w64, top(dy), top(w))),
+            (dw, lambda h, d: loss(x64, w64 + h * d), w64,
+             slack(dy.double().t(), x64, top(dy), top(x)))):
+        d = torch.sign(grad.double())
+        h = 1e-3
+        diff = (along(h, d) - along(-h, d)) / (2 * h)
+        assert abs(float(diff - (grad.double() * d).sum())) <= float(tol.sum()) * (1 + 1e-4)
+
+
+# ---------------------------------------------------------------- grouped product
+
+def _grouped_case(T, E, k, N, K, bm, seed=0, ids=None):
+    if ids is None:
+        ids = _rand(T, E, seed=seed).topk(k, 1).indices.to(torch.int32)
+    al = ops.align(ids.contiguous(), E, bm)
+    w = ops.fp8_quant(_rand(E, N, K, seed=seed + 1, scale=K ** -0.5), block=True)
+    return ids, al, w["codes"], w["scale"]
+
+
+def _grouped_check(out, ids, a, sa, b, sb, k, pair_rows, K):
+    E = b.shape[0]
+    av = R.wide(a, sa)
+    flat = ids.reshape(-1)
+    for e in range(E):
+        p = (flat == e).nonzero().reshape(-1)
+        if p.numel():
+            _close(out[p], av[p if pair_rows else p // k], R.wide(b[e], sb[e], True), K)
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128])
+@pytest.mark.parametrize("T,E,k,N,K", [(1, 8, 2, 128, 128), (1, 1, 1, 5, 128), (4, 128, 8, 192, 256),
+                                       (33, 16, 4, 257, 384), (100, 4, 2, 640, 256),
+                                       (700, 8, 3, 130, 512), (2000, 3, 1, 513, 128)])
+def test_grouped_matmul(T, E, k, N, K, bm):
+    print(f"grouped {T} {E} {k} {N} {K} {bm}", flush=True)
+    ids, al, b, sb = _grouped_case(T, E, k, N, K, bm, seed=T)
+    for pair_rows in (False, True):
+        q = ops.fp8_quant(_rand(T * k if pair_rows else T, K, seed=9))
+        for dt in (BF, F32):
+            out = torch.full((T * k, N), float("nan"), dtype=dt, device="cuda")
+            ops.fp8_grouped_matmul(q["codes"], q["scale"], b, sb, al, k, pair_rows=pair_rows,
+                                   out_dtype=dt, out=out)
+            _grouped_check(out, ids, q["codes"], q["scale"], b, sb, k, pair_rows, K)
+            again = ops.fp8_grouped_matmul(q["codes"], q["scale"], b, sb, al, k,
+                                           pair_rows=pair_rows, out_dtype=dt)
+            assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("bm", [16, 32, 64, 128])
+def test_grouped_matmul_one_expert_takes_all_and_dropped_pairs_stay(bm):
+    T, E, k, N, K = 150, 8, 2, 200, 256
+    ids = torch.empty(T, k, dtype=torch.int32, device="cuda")
+    ids[:, 0], ids[:, 1] = 5, 2
+    ids[7] = torch.tensor([E + 4, -1], dtype=torch.int32, device="cuda")  # dropped by align
+    ids, al, b, sb = _grouped_case(T, E, k, N, K, bm, ids=ids)
+    q = ops.fp8_quant(_rand(T, K, seed=3))
+    out = torch.full((T * k, N), 11.0, dtype=BF, device="cuda")
+    ops.fp8_grouped_matmul(q["codes"], q["scale"], b, sb, al, k, out=out)
+    _grouped_check(out, ids, q["codes"], q["scale"], b, sb, k, False, K)
+    assert (out[14:16] == 11).all()
+
+
+def test_grouped_matmul_refuses_what_does_not_fit():
+    ids, al, b, sb = _grouped_case(20, 4, 2, 64, 128, 16)
+    q = ops.fp8_quant(_rand(20, 128))
+    ok = (q["codes"], q["scale"], b, sb, al, 2)
+    ops.fp8_grouped_matmul(*ok)
+    for i, wrong in ((0, q["codes"][:19].contiguous()), (1, q["scale"].t().contiguous()),
+                     (2, b[0]), (3, sb[:3].contiguous()), (4, {**al, "block_m": 32}), (5, 3),
+                     (4, {**al, "num_padded": al["num_padded"].float()})):
+        with pytest.raises(ValueError):
+            ops.fp8_grouped_matmul(*ok[:i], wrong, *ok[i + 1:])
+    with pytest.raises(ValueError):
+        ops.fp8_grouped_matmul(*ok, out=torch.empty(40, 64, dtype=F32, device="cuda"))
+    with pytest.raises(ValueError):
+        ops.fp8_matmul(q["codes"].t().contiguous().t(), q["scale"], b[0], sb[0])  # not contiguous
+
+
+# ---------------------------------------------------------------- balance loss
+
+def _balance_tol(z, T):
+    """Relative error of a softmax sum in fp32: z - max is off by half a step
+    of its size, exp by 2 ulp, a row's sum by its depth (16 + 8 steps), the
+    division and the sum over a wave's tokens (at most T / 4 + 4 steps)."""
+    span = float((z[z.isfinite()].max() - z[z.isfinite()].min()).abs()) if z.isfinite().any() else 0
+    return (span + 4 + 24 + 2 + min(T, T / 4 + 4) + 4) * R.U32
+
+
+@pytest.mark.parametrize("masked", ["none", "some", "all", "bool"])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 65, 5), (64, 8, 2), (63, 128, 8),
+                                   (257, 200, 16), (1000, 512, 10), (4100, 60, 4), (999, 1024, 16)])
+def test_balance(T, E, k, masked):
+    z = _rand(T, E, seed=T + E, scale=2.0)
+    ids = z.topk(k, 1).indices.to(torch.int32)
+    if T > 2:
+        ids[2] = -1          # a dropped token's picks
+        ids[1, 0] = E        # out of range: not counted
+        ids[0, :] = ids[0, 0]  # the same index k times: counted k times
+    mask = None
+    if masked != "none":
+        mask = _rand(T, seed=7) < 0.7
+        if masked == "all":
+            mask[:] = False
+        if masked != "bool":
+            mask = mask.to(torch.uint8) * 3  # any nonzero byte keeps
+        z[~mask.bool()] = float("nan")  # what a mask drops is not read
+    coef = 0.37
+    f = ops.balance_loss(z, ids, mask=mask, coef=coef)
+    loss, counts, probs, n = R.balance(z, ids, mask, coef)
+    rel = _balance_tol(z, T)
+    assert torch.equal(f["counts"].long(), counts) and int(f["tokens"]) == n
+    assert ((f["probs"].double() - probs).abs() <= probs * rel + 1e-37).all()
+    # a sum of terms that are not negative, each off by rel, rounded once
+    assert abs(float(f["loss"]) - float(loss)) <= float(loss) * (rel + 2 * R.U32)
+    again = ops.balance_loss(z, ids, mask=mask, coef=coef)
+    assert all(torch.equal(again[key], f[key]) for key in f)
+
+    up = torch.tensor([1.7], device="cuda")
+    dz = ops.balance_loss_backward(z, f["counts"], f["tokens"], k, up, mask=mask, coef=coef)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda") if mask is None else mask.bool()
+    assert not dz[~keep].any()
+    if n == 0:
+        return
+    p = R.softmax(z[keep])
+    fr = counts.double() / (k * n)
+    g = float(up.double()) * coef * E / n
+    ref = g * p * (fr - (p * fr).sum(1, keepdim=True))
+    # p off by rel; f, the row's dot product (24 steps) and their difference by
+    # half steps of f + dot; three products
+    tol = g * p * (fr + (p * fr).sum(1, keepdim=True)) * (2 * rel + 32 * R.U32) + 1e-37
+    assert ((dz[keep].double() - ref).abs() <= tol).all()
+    # differences of the 64-bit loss, the counts held
+    d = _rand(T, E, seed=3).double()
+    zk, dk, h = z[keep].double(), d[keep], 1e-4
+
+    def total(zz):
+        return coef * E * (fr * (R.softmax(zz).sum(0) / n)).sum()
+    diff = float(up.double()) * (total(zk + h * dk) - total(zk - h * dk)) / (2 * h)
+    # third derivatives of softmax are below 6 |d|^3 in size: h^2 g (f p |d|^3)
+    third = h * h * g * float((p * fr * (dk.abs() ** 3).amax(1, keepdim=True)).sum()) * 6
+    assert abs(float(diff - (dz[keep].double() * dk).sum())) <= \
+        float((tol * dk.abs()).sum()) + third + 1e-9 * float(total(zk)) / h * 1e-3
+
+
+def test_balance_masked_experts_and_rows_without_any():
+    T, E, k = 40, 70, 3
+    z = _rand(T, E, seed=1)
+    z[:, 10:20] = -float("inf")
+    z[5] = -float("inf")
+    z[6] = torch.finfo(F32).min
+    ids = z.nan_to_num(neginf=-1e30).topk(k, 1).indices.to(torch.int32)
+    f = ops.balance_loss(z, ids, coef=1.0)
+    loss, counts, probs, n = R.balance(z, ids, None, 1.0)
+    rel = _balance_tol(z[7:], T)
+    assert torch.equal(f["counts"].long(), counts) and int(f["tokens"]) == T
+    assert ((f["probs"].double() - probs).abs() <= probs * rel).all()
+    # row 6, whose logits are all the lowest finite number, is uniform over all E
+    assert ((f["probs"][10:20].double() - 1 / (E * T)).abs() <= rel / (E * T)).all()
+    assert abs(float(f["loss"]) - float(loss)) <= float(loss) * (rel + 2 * R.U32)
+    one = torch.ones(1, device="cuda")
+    dz = ops.balance_loss_backward(z, f["counts"], f["tokens"], k, one)
+    assert torch.isfinite(dz).all() and not dz[5].any()
+    assert not dz[torch.arange(T) != 6, 10:20].any()
+    z[9, 3] = float("nan")
+    f = ops.balance_loss(z, ids)
+    assert f["loss"].isnan().all() and torch.equal(f["counts"].long(), counts)
+
+
+def test_balance_in_place_and_empty():
+    z = _rand(50, 33, seed=4)
+    ids = z.topk(2, 1).indices.to(torch.int32)
+    f = ops.balance_loss(z, ids)
+    one = torch.ones(1, device="cuda")
+    dz = ops.balance_loss_backward(z, f["counts"], f["tokens"], 2, one)
+    buf = z.clone()
+    assert torch.equal(ops.balance_loss_backward(buf, f["counts"], f["tokens"], 2, one, out=buf), dz)
+    f = ops.balance_loss(z[:0], ids[:0])
+    assert float(f["loss"]) == 0 and not f["counts"].any() and not f["probs"].any()
+    assert int(f["tokens"]) == 0
