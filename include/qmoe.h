@@ -390,7 +390,7 @@ qmoe_status qmoe_fp8_quant(const void* x, int32_t dtype, int32_t B, int32_t M, i
  * ws: qmoe_fp8_matmul_workspace(M, N, K) bytes (0: none needed, ws may be
  *   NULL), 256-byte aligned, contents need no initialisation; calls that
  *   share it must be ordered on one stream.  a, b: 16-byte aligned.
- * Limits: M, N, K <= 2^24 (QMOE_ERR_UNSUPPORTED).                        */
+ * Limits: M, N <= 2^24, K <= 2^22 (QMOE_ERR_UNSUPPORTED).                */
 size_t qmoe_fp8_matmul_workspace(int32_t M, int32_t N, int32_t K);
 qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_t* b,
                             const float* b_scale, int32_t b_block, int32_t M, int32_t N,
@@ -407,7 +407,8 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
  * sorted_pair_ids, tile_expert, num_padded: qmoe_align's outputs for the
  *   same T, k, E and block_m.  out [T*k, N] bf16 or fp32; rows of pairs that
  *   qmoe_align dropped are left as they are.
- * K % 128 == 0, any N; E <= 1024.                                        */
+ * K % 128 == 0, any N; E <= 1024, a below 4 GiB, N <= 2^24, K <= 2^22
+ * (QMOE_ERR_UNSUPPORTED).                                                 */
 qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int32_t pair_rows,
                                     const uint8_t* b, const float* b_scale,
                                     const int32_t* sorted_pair_ids, const int32_t* tile_expert,

@@ -31,6 +31,9 @@ BalanceWs balance_ws_layout(int T, int E) {
   return w;
 }
 
+// A tile's rows of K bytes are addressed with 31-bit byte offsets.
+constexpr int kMaxK = 1 << 22;
+
 bool valid_form(int32_t form) { return form >= QMOE_FORM_BF16 && form <= QMOE_FORM_E4M3_B128; }
 bool form_scaled(int32_t form) { return form >= QMOE_FORM_INT8; }
 // `arrays`: those of H columns (nullptr for one that is not given).
@@ -82,7 +85,7 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
   if (M < 0 || N < 1 || K < 128 || K % 128 != 0 || b_block < 0 || b_block > 1 ||
       !valid_dtype(out_dtype))
     return QMOE_ERR_INVALID_ARG;
-  if (M > (1 << 24) || N > (1 << 24) || K > (1 << 24)) return QMOE_ERR_UNSUPPORTED;
+  if (M > (1 << 24) || N > (1 << 24) || K > kMaxK) return QMOE_ERR_UNSUPPORTED;
   if (M == 0) return QMOE_OK;
   if (!a || !a_scale || !b || !b_scale || !out) return QMOE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) ||
@@ -119,7 +122,9 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
   if (block_m != 16 && block_m != 32 && block_m != 64 && block_m != 128)
     return QMOE_ERR_INVALID_ARG;
   if ((long long)T * k > (1ll << 30)) return QMOE_ERR_INVALID_ARG;
-  if (E > 1024 || N > (1 << 24) || K > (1 << 24)) return QMOE_ERR_UNSUPPORTED;
+  if (E > 1024 || N > (1 << 24) || K > kMaxK) return QMOE_ERR_UNSUPPORTED;
+  // Gathered rows are addressed with 32-bit byte offsets.
+  if ((uint64_t)T * (pair_rows ? k : 1) * K >= (1ull << 32)) return QMOE_ERR_UNSUPPORTED;
   if (T == 0) return QMOE_OK;
   if (!a || !a_scale || !b || !b_scale || !sorted_pair_ids || !tile_expert || !num_padded || !out)
     return QMOE_ERR_INVALID_ARG;

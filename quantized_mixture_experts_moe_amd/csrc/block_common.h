@@ -80,6 +80,16 @@ __device__ inline void store8(void* p, size_t i, const float v[8]) {
   }
 }
 
+// Four consecutive values (the byte address a multiple of their size).
+template <bool F32>
+__device__ inline void store4(void* p, size_t i, const float v[4]) {
+  if constexpr (F32)
+    *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
+  else
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p) + i) =
+        u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
 // x of the lane that DPP control CTRL names.
 template <int CTRL>
 __device__ inline uint32_t dpp(uint32_t x) {

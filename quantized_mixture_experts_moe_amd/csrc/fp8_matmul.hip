@@ -140,11 +140,309 @@ __global__ __launch_bounds__(256) void fp8_matmul_rows16_kernel(Fp8MatmulArgs g)
     }
 }
 
+// ---------------------------------------------------------------------------
+// Tiled kernel: a block of WM x WN waves computes BM rows x BN columns, a
+// wave SM x SN sub-tiles of 32 x 32.  Both operands' K blocks (128 bytes per
+// row) go from memory straight into LDS, two stages; a row's eight 16-byte
+// chunks are stored in the order c ^ (row / 2 % 8), so that the 16 rows that
+// are read together lie in different banks (the permutation is applied to the
+// memory addresses: the copy writes LDS in lane order).
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Buffer descriptor of `bytes` bytes at p (raw, no swizzle); reads behind the
+// end give zeros.
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ inline Rsrc rsrc(const void* p, size_t bytes) {
+  const unsigned n = bytes < 0xfffffff0u ? (unsigned)bytes : 0xfffffff0u;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)n, 0x00027000);
+}
+// 16 bytes per lane from voff (per lane) + soff (the wave's) to LDS, in lane
+// order.
+__device__ inline void copy16(Rsrc r, unsigned voff, unsigned soff, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
+                                           (int)voff, (int)soff, 0, 0);
+}
+__device__ inline void copy4(Rsrc r, unsigned voff, float* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
+                                           (int)voff, 0, 0, 0);
+}
+__device__ inline float load_f32(Rsrc r, unsigned voff) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, 0, 0));
+}
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+  static constexpr int SM = BM / WM / 32, SN = BN / WN / 32;
+  static constexpr int AC = BM / 8 / WAVES, BC = BN / 8 / WAVES;  // copies per wave and K block
+  static_assert(SM * WM * 32 == BM && SN * WN * 32 == BN, "whole sub-tiles");
+  static_assert(AC * WAVES * 8 == BM && BC * WAVES * 8 == BN, "whole copies");
+};
+
+template <class C, bool GROUPED, bool BBLOCK, bool F32>
+__global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8MatmulArgs g) {
+  constexpr int SM = C::SM, SN = C::SN;
+  __shared__ float c0[BBLOCK ? 1 : C::BN], c1[BBLOCK ? 1 : C::BN];  // b's row scales
+  __shared__ uint8_t a0[C::BM * 128], b0[C::BN * 128], a1[C::BM * 128], b1[C::BN * 128];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wm = wave % C::WM, wn = wave / C::WM;
+  const int ntn = (g.N + C::BN - 1) / C::BN;
+  const int ntm = ((GROUPED ? *g.num_padded : g.M) + C::BM - 1) / C::BM;
+  // The launch order deals blocks to the XCDs in turn: give each XCD a
+  // contiguous run of tiles, column-tile by column-tile inside bands of
+  // kBand row tiles, so that its L2 sees the same rows again.
+  constexpr int kBand = 8;
+  const int total = ntn * ntm, per = (total + 7) / 8;
+  const int id = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (id >= total || (int)(blockIdx.x / 8) >= per) return;  // also past the tiles in use
+  const int band = id / (kBand * ntn), in = id - band * kBand * ntn;
+  const int rows = min(kBand, ntm - band * kBand);
+  const int m0 = (band * kBand + in % rows) * C::BM, n0 = in / rows * C::BN;
+  const uint8_t* b = g.b;
+  const float* bs = g.b_scale;
+  if constexpr (GROUPED) {
+    const int e = g.tile_expert[m0 / g.block_m];
+    if (e < 0) return;
+    b += (size_t)e * g.N * g.K;
+    bs += (size_t)e * ((g.N + 127) / 128) * g.KB;
+  }
+  // Copies: 8 lanes per row, the rows of a wave's copy t being 8 t .. 8 t + 7.
+  // The chunk order alternates with t, hence two lane offsets where the rows
+  // are consecutive; gathered rows have one per copy.
+  const size_t K = g.K;
+  auto swz = [&](int t) { return 16u * ((lane & 7) ^ ((4 * t + (lane >> 4)) & 7)); };
+  const Rsrc ra = GROUPED ? rsrc(g.a, (size_t)g.Ma * K)
+                          : rsrc(g.a + (size_t)m0 * K, (size_t)(g.M - m0) * K);
+  const Rsrc rb = rsrc(b + (size_t)n0 * K, (size_t)(g.N - n0) * K);
+  unsigned av[GROUPED ? C::AC : 2];
+  const unsigned bv[2] = {(lane >> 3) * (unsigned)g.K + swz(0), (lane >> 3) * (unsigned)g.K + swz(1)};
+  if constexpr (GROUPED) {
+#pragma unroll
+    for (int i = 0; i < C::AC; i++) {
+      const int t = wave * C::AC + i;
+      const int row = Rows<true>::a_row(g, Rows<true>::out_row(g, m0 + t * 8 + (lane >> 3)));
+      av[i] = (unsigned)row * (unsigned)g.K + swz(t);
+    }
+  } else {
+    av[0] = bv[0];
+    av[1] = bv[1];
+  }
+  // Scales of the lane's rows, one K block ahead.
+  const int r32 = lane & 31, h = lane >> 5;
+  int orow[SM];
+  unsigned so[SM];
+#pragma unroll
+  for (int s = 0; s < SM; s++) {
+    orow[s] = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + r32);
+    so[s] = 4u * (unsigned)Rows<GROUPED>::a_row(g, orow[s]);
+  }
+  const int nw = n0 + wn * SN * 32;  // the wave's first column
+  const float* sbp = bs + (BBLOCK ? (size_t)(min(nw, g.N - 1) / 128) * g.KB : 0);
+  float sa[SM], nsa[SM], nsb = 1.0f;  // of this K block, of the next one
+  auto take = [&]() {
+#pragma unroll
+    for (int s = 0; s < SM; s++) sa[s] = nsa[s] * nsb;
+  };
+  auto load = [&](uint8_t* la, uint8_t* lb, float* lc, int kb) {
+    const Rsrc rs = rsrc(g.a_scale + (size_t)kb * g.Ma, (size_t)g.Ma * 4);
+#pragma unroll
+    for (int s = 0; s < SM; s++) nsa[s] = load_f32(rs, so[s]);
+    if constexpr (BBLOCK) {
+      nsb = load_f32(rsrc(sbp + kb, 4), 0);
+    } else if (wave < C::BN / 64) {
+      const Rsrc rc = rsrc(bs + (size_t)kb * g.N + n0, (size_t)(g.N - n0) * 4);
+      copy4(rc, wave * 256 + lane * 4, lc + wave * 64);
+    }
+#pragma unroll
+    for (int i = 0; i < C::AC; i++) {
+      const int t = wave * C::AC + i;
+      if constexpr (GROUPED)
+        copy16(ra, av[i], kb * 128, la + t * 1024);
+      else
+        copy16(ra, (C::AC % 2 == 0 ? i : t) % 2 ? av[1] : av[0], t * 8 * g.K + kb * 128,
+               la + t * 1024);
+    }
+#pragma unroll
+    for (int i = 0; i < C::BC; i++) {
+      const int t = wave * C::BC + i;
+      copy16(rb, (C::BC % 2 == 0 ? i : t) % 2 ? bv[1] : bv[0], t * 8 * g.K + kb * 128,
+             lb + t * 1024);
+    }
+  };
+  // Reads: lane's row in a sub-tile and its half of each 64 positions of K.
+  int off[2][2];
+#pragma unroll
+  for (int j = 0; j < 2; j++)
+#pragma unroll
+    for (int e = 0; e < 2; e++)
+      off[j][e] = r32 * 128 + 16 * ((4 * j + 2 * h + e) ^ ((r32 >> 1) & 7));
+  f32x16 acc[SN][SM];
+#pragma unroll
+  for (int i = 0; i < SN; i++)
+#pragma unroll
+    for (int s = 0; s < SM; s++)
+#pragma unroll
+      for (int r = 0; r < 16; r++) acc[i][s][r] = 0.f;
+
+  auto frag = [&](const uint8_t* t, int sub, int j) {
+    return join(*reinterpret_cast<const u32x4*>(t + sub * 4096 + off[j][0]),
+                *reinterpret_cast<const u32x4*>(t + sub * 4096 + off[j][1]));
+  };
+  f32x4 sbn[BBLOCK ? 1 : SN][4];  // b's scales of the lane's 16 columns per sub-tile
+  auto row_scales = [&](const float* lc) {
+    if constexpr (!BBLOCK) {
+#pragma unroll
+      for (int i = 0; i < SN; i++)
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+          sbn[i][q] =
+              *reinterpret_cast<const f32x4*>(lc + (wn * SN + i) * 32 + 8 * q + 4 * h);
+    }
+  };
+  auto scaled = [&](const f32x16& t, int i, int s) {
+#pragma unroll
+    for (int r = 0; r < 16; r++) {
+      if constexpr (BBLOCK)
+        acc[i][s][r] = __builtin_fmaf(t[r], sa[s], acc[i][s][r]);
+      else
+        acc[i][s][r] = __builtin_fmaf(t[r] * sbn[i][r >> 2][r & 3], sa[s], acc[i][s][r]);
+    }
+  };
+  auto compute = [&](const uint8_t* la, const uint8_t* lb, const float* lc) {
+    row_scales(lc);
+    if constexpr (F32) {
+      // The codes widened to bf16, 16 positions of K per instruction: a lane's
+      // chunk of 16 codes feeds two.
+      f32x16 t[SN][SM];
+#pragma unroll
+      for (int i = 0; i < SN; i++)
+#pragma unroll
+        for (int s = 0; s < SM; s++)
+#pragma unroll
+          for (int r = 0; r < 16; r++) t[i][s][r] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 4; c++) {
+        const int o = r32 * 128 + 16 * ((2 * c + h) ^ ((r32 >> 1) & 7));
+        u32x4 x[SM], y[SN];
+#pragma unroll
+        for (int i = 0; i < SN; i++)
+          y[i] = *reinterpret_cast<const u32x4*>(lb + (wn * SN + i) * 4096 + o);
+#pragma unroll
+        for (int s = 0; s < SM; s++)
+          x[s] = *reinterpret_cast<const u32x4*>(la + (wm * SM + s) * 4096 + o);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          bf16x8 xs[SM];
+#pragma unroll
+          for (int s = 0; s < SM; s++) xs[s] = widen8(x[s][2 * j], x[s][2 * j + 1]);
+#pragma unroll
+          for (int i = 0; i < SN; i++) {
+            const bf16x8 ys = widen8(y[i][2 * j], y[i][2 * j + 1]);
+#pragma unroll
+            for (int s = 0; s < SM; s++)
+              t[i][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ys, xs[s], t[i][s], 0, 0, 0);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < SN; i++)
+#pragma unroll
+        for (int s = 0; s < SM; s++) scaled(t[i][s], i, s);
+    } else {
+      i32x8 bf[SN][2];
+#pragma unroll
+      for (int i = 0; i < SN; i++)
+#pragma unroll
+        for (int j = 0; j < 2; j++) bf[i][j] = frag(lb, wn * SN + i, j);
+      f32x16 t[2];
+#pragma unroll
+      for (int s = 0; s < SM; s++) {
+        const i32x8 x0 = frag(la, wm * SM + s, 0), x1 = frag(la, wm * SM + s, 1);
+#pragma unroll
+        for (int i = 0; i < SN; i++) {
+          const int q = s * SN + i;
+          f32x16 z;
+#pragma unroll
+          for (int r = 0; r < 16; r++) z[r] = 0.f;
+          z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[i][0], x0, z, 0, 0, 0, kUnit, 0,
+                                                              kUnit);
+          z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[i][1], x1, z, 0, 0, 0, kUnit, 0,
+                                                              kUnit);
+          t[q & 1] = z;
+          // The scaling of the sub-tile before runs while the matrix core works.
+          if (q > 0) scaled(t[(q - 1) & 1], (q - 1) % SN, (q - 1) / SN);
+        }
+      }
+      scaled(t[(SM * SN - 1) & 1], SN - 1, SM - 1);
+    }
+  };
+  load(a0, b0, c0, 0);
+  for (int kb = 0; kb < g.KB; kb += 2) {
+    __syncthreads();  // stage 0 has landed, stage 1 is free
+    take();
+    if (kb + 1 < g.KB) load(a1, b1, c1, kb + 1);
+    compute(a0, b0, c0);
+    if (kb + 1 >= g.KB) break;
+    __syncthreads();
+    take();
+    if (kb + 2 < g.KB) load(a0, b0, c0, kb + 2);
+    compute(a1, b1, c1);
+  }
+  // A lane holds four times four consecutive columns of its row per sub-tile.
+  const bool wide = g.N % 4 == 0 && (uintptr_t)g.out % (F32 ? 16 : 8) == 0;
+#pragma unroll
+  for (int s = 0; s < SM; s++) {
+    if (orow[s] < 0) continue;
+    const size_t o = (size_t)orow[s] * g.N;
+#pragma unroll
+    for (int i = 0; i < SN; i++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int n = nw + i * 32 + 8 * q + 4 * h;
+        const float v[4] = {acc[i][s][4 * q], acc[i][s][4 * q + 1], acc[i][s][4 * q + 2],
+                            acc[i][s][4 * q + 3]};
+        if (wide) {
+          if (n < g.N) store4<F32>(g.out, o + n, v);
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; r++)
+            if (n + r < g.N) store1<F32>(g.out, o + n + r, v[r]);
+        }
+      }
+  }
+}
+
+template <class C, bool GROUPED, bool BBLOCK, bool F32>
+hipError_t launch_tile(const Fp8MatmulArgs& g, hipStream_t s) {
+  const long long total =
+      (long long)((g.N + C::BN - 1) / C::BN) * ((g.M + C::BM - 1) / C::BM);
+  if (total > (1ll << 30)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, F32>),
+                     dim3((unsigned)((total + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 size_t fp8_matmul_parts_bytes(int, int, int) { return 0; }
 
+// Rows up to which the untiled kernel is taken.
+constexpr int kFewRows = 32;
+
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
+  typedef Tile<128, 128, 2, 2> Mid;
+  typedef Tile<256, 256, 2, 4> Big;
+  if (g.M >= kFewRows) {
+    if (g.out_f32)
+      return g.b_block ? launch_tile<Mid, false, true, true>(g, s)
+                       : launch_tile<Mid, false, false, true>(g, s);
+    if (!g.b_block) return launch_tile<Mid, false, false, false>(g, s);
+    const long long big = (long long)((g.M + 255) / 256) * ((g.N + 255) / 256);
+    return big >= 200 ? launch_tile<Big, false, true, false>(g, s)
+                      : launch_tile<Mid, false, true, false>(g, s);
+  }
   const dim3 grid((g.N + 255) / 256, (g.M + 15) / 16), block(256);
 #define QMOE_CALL(BB, F32) \
   hipLaunchKernelGGL((fp8_matmul_rows16_kernel<false, BB, F32>), grid, block, 0, s, g)
@@ -160,13 +458,20 @@ hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_fp8_grouped_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
+namespace {
+template <bool F32>
+hipError_t grouped(const Fp8MatmulArgs& g, hipStream_t s) {
+  if (g.block_m == 128) return launch_tile<Tile<128, 128, 2, 2>, true, true, F32>(g, s);
+  if (g.block_m == 64) return launch_tile<Tile<64, 128, 1, 4>, true, true, F32>(g, s);
+  if (g.block_m == 32) return launch_tile<Tile<32, 128, 1, 4>, true, true, F32>(g, s);
   const dim3 grid((g.N + 255) / 256, (g.M + 15) / 16), block(256);
-  if (g.out_f32)
-    hipLaunchKernelGGL((fp8_matmul_rows16_kernel<true, true, true>), grid, block, 0, s, g);
-  else
-    hipLaunchKernelGGL((fp8_matmul_rows16_kernel<true, true, false>), grid, block, 0, s, g);
+  hipLaunchKernelGGL((fp8_matmul_rows16_kernel<true, true, F32>), grid, block, 0, s, g);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_fp8_grouped_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
+  return g.out_f32 ? grouped<true>(g, s) : grouped<false>(g, s);
 }
 
 }  // namespace qmoe
