@@ -170,6 +170,14 @@ __device__ inline float load_f32(Rsrc r, unsigned voff) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, 0, 0));
 }
 
+// Waits for the wave's copies (vmcnt 0; the barrier alone does not wait for
+// copies to LDS), then for the other waves'.
+__device__ inline void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+__device__ inline void landed() {
+  wait_copies();
+  __syncthreads();
+}
+
 template <int BM_, int BN_, int WM_, int WN_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -213,9 +221,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   // are consecutive; gathered rows have one per copy.
   const size_t K = g.K;
   auto swz = [&](int t) { return 16u * ((lane & 7) ^ ((4 * t + (lane >> 4)) & 7)); };
-  const Rsrc ra = GROUPED ? rsrc(g.a, (size_t)g.Ma * K)
-                          : rsrc(g.a + (size_t)m0 * K, (size_t)(g.M - m0) * K);
-  const Rsrc rb = rsrc(b + (size_t)n0 * K, (size_t)(g.N - n0) * K);
+  const uint8_t* abase = GROUPED ? g.a : g.a + (size_t)m0 * K;
+  const uint8_t* bbase = b + (size_t)n0 * K;
+  const size_t abytes = (GROUPED ? (size_t)g.Ma : (size_t)(g.M - m0)) * K;
+  const size_t bbytes = (size_t)(g.N - n0) * K;
   unsigned av[GROUPED ? C::AC : 2];
   const unsigned bv[2] = {(lane >> 3) * (unsigned)g.K + swz(0), (lane >> 3) * (unsigned)g.K + swz(1)};
   if constexpr (GROUPED) {
@@ -245,28 +254,33 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
 #pragma unroll
     for (int s = 0; s < SM; s++) sa[s] = nsa[s] * nsb;
   };
-  auto load = [&](uint8_t* la, uint8_t* lb, float* lc, int kb) {
-    const Rsrc rs = rsrc(g.a_scale + (size_t)kb * g.Ma, (size_t)g.Ma * 4);
+  // (K blocks behind the last one are copies of nothing: empty buffers.)
+  auto load_scales = [&](float* lc, int kb) {
+    const bool any = kb < g.KB;
+    const Rsrc rs = rsrc(g.a_scale + (size_t)kb * g.Ma, any ? (size_t)g.Ma * 4 : 0);
 #pragma unroll
     for (int s = 0; s < SM; s++) nsa[s] = load_f32(rs, so[s]);
     if constexpr (BBLOCK) {
-      nsb = load_f32(rsrc(sbp + kb, 4), 0);
+      nsb = load_f32(rsrc(sbp + kb, any ? 4 : 0), 0);
     } else if (wave < C::BN / 64) {
-      const Rsrc rc = rsrc(bs + (size_t)kb * g.N + n0, (size_t)(g.N - n0) * 4);
+      const Rsrc rc = rsrc(bs + (size_t)kb * g.N + n0, any ? (size_t)(g.N - n0) * 4 : 0);
       copy4(rc, wave * 256 + lane * 4, lc + wave * 64);
     }
-#pragma unroll
-    for (int i = 0; i < C::AC; i++) {
-      const int t = wave * C::AC + i;
+  };
+  // Copy c of the wave's AC + BC ones of a K block.
+  auto load = [&](uint8_t* la, uint8_t* lb, int kb, int c) {
+    const bool any = kb < g.KB;
+    if (c < C::AC) {
+      const int t = wave * C::AC + c;
+      const Rsrc ra = rsrc(abase, any ? abytes : 0);
       if constexpr (GROUPED)
-        copy16(ra, av[i], kb * 128, la + t * 1024);
+        copy16(ra, av[c], kb * 128, la + t * 1024);
       else
-        copy16(ra, (C::AC % 2 == 0 ? i : t) % 2 ? av[1] : av[0], t * 8 * g.K + kb * 128,
+        copy16(ra, (C::AC % 2 == 0 ? c : t) % 2 ? av[1] : av[0], t * 8 * g.K + kb * 128,
                la + t * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < C::BC; i++) {
-      const int t = wave * C::BC + i;
+    } else {
+      const int i = c - C::AC, t = wave * C::BC + i;
+      const Rsrc rb = rsrc(bbase, any ? bbytes : 0);
       copy16(rb, (C::BC % 2 == 0 ? i : t) % 2 ? bv[1] : bv[0], t * 8 * g.K + kb * 128,
              lb + t * 1024);
     }
@@ -310,8 +324,13 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
         acc[i][s][r] = __builtin_fmaf(t[r] * sbn[i][r >> 2][r & 3], sa[s], acc[i][s][r]);
     }
   };
-  auto compute = [&](const uint8_t* la, const uint8_t* lb, const float* lc) {
+  // One K block from LDS; the next one's copies (to na, nb) are issued between
+  // the matrix instructions, so that no wave waits in front of them for the
+  // memory pipe to take its copies.
+  auto compute = [&](const uint8_t* la, const uint8_t* lb, const float* lc, uint8_t* na, uint8_t* nb,
+                     float* nc, int kb) {
     row_scales(lc);
+    load_scales(nc, kb + 1);
     if constexpr (F32) {
       // The codes widened to bf16, 16 positions of K per instruction: a lane's
       // chunk of 16 codes feeds two.
@@ -332,6 +351,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
 #pragma unroll
         for (int s = 0; s < SM; s++)
           x[s] = *reinterpret_cast<const u32x4*>(la + (wm * SM + s) * 4096 + o);
+#pragma unroll
+        for (int u = c * (C::AC + C::BC) / 4; u < (c + 1) * (C::AC + C::BC) / 4; u++)
+          load(na, nb, kb + 1, u);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
           bf16x8 xs[SM];
@@ -371,6 +393,10 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
           z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[i][1], x1, z, 0, 0, 0, kUnit, 0,
                                                               kUnit);
           t[q & 1] = z;
+          constexpr int kParts = (SM * SN + 1) / 2;  // all copies by the middle of the step
+#pragma unroll
+          for (int u = 0; u < C::AC + C::BC; u++)
+            if (u * kParts / (C::AC + C::BC) == q) load(na, nb, kb + 1, u);
           // The scaling of the sub-tile before runs while the matrix core works.
           if (q > 0) scaled(t[(q - 1) & 1], (q - 1) % SN, (q - 1) / SN);
         }
@@ -378,18 +404,19 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
       scaled(t[(SM * SN - 1) & 1], SN - 1, SM - 1);
     }
   };
-  load(a0, b0, c0, 0);
+  load_scales(c0, 0);
+#pragma unroll
+  for (int u = 0; u < C::AC + C::BC; u++) load(a0, b0, 0, u);
   for (int kb = 0; kb < g.KB; kb += 2) {
-    __syncthreads();  // stage 0 has landed, stage 1 is free
+    landed();  // stage 0 is there, stage 1 is free
     take();
-    if (kb + 1 < g.KB) load(a1, b1, c1, kb + 1);
-    compute(a0, b0, c0);
+    compute(a0, b0, c0, a1, b1, c1, kb);
     if (kb + 1 >= g.KB) break;
-    __syncthreads();
+    landed();
     take();
-    if (kb + 2 < g.KB) load(a0, b0, c0, kb + 2);
-    compute(a1, b1, c1);
+    compute(a1, b1, c1, a0, b0, c0, kb + 1);
   }
+  wait_copies();  // no copy outlives the block's LDS
   // A lane holds four times four consecutive columns of its row per sub-tile.
   const bool wide = g.N % 4 == 0 && (uintptr_t)g.out % (F32 ? 16 : 8) == 0;
 #pragma unroll
