@@ -192,7 +192,11 @@ template <class C, bool GROUPED, bool BBLOCK, bool F32>
 __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8MatmulArgs g) {
   constexpr int SM = C::SM, SN = C::SN;
   __shared__ float c0[BBLOCK ? 1 : C::BN], c1[BBLOCK ? 1 : C::BN];  // b's row scales
-  __shared__ uint8_t a0[C::BM * 128], b0[C::BN * 128], a1[C::BM * 128], b1[C::BN * 128];
+  __shared__ __align__(1024) uint8_t lds[2 * (C::BM + C::BN) * 128];
+  uint8_t* const a0 = lds;
+  uint8_t* const b0 = a0 + C::BM * 128;
+  uint8_t* const a1 = b0 + C::BN * 128;
+  uint8_t* const b1 = a1 + C::BM * 128;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
@@ -418,7 +422,45 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   }
   wait_copies();  // no copy outlives the block's LDS
   // A lane holds four times four consecutive columns of its row per sub-tile.
-  const bool wide = g.N % 4 == 0 && (uintptr_t)g.out % (F32 ? 16 : 8) == 0;
+  // Where rows can be stored in 16-byte pieces, each wave turns its tile over
+  // in LDS, 32 rows at a time, so that consecutive lanes store consecutive
+  // bytes (the pieces of a row in the order p ^ row % 8, against bank
+  // conflicts).
+  constexpr int EB = F32 ? 4 : 2;             // bytes per value
+  constexpr int RB = SN * 32 * EB;            // bytes per row of the wave's tile
+  constexpr int PIECES = RB / 16, RPI = 64 / PIECES;  // pieces per row, rows per store
+  static_assert(C::WAVES * 32 * RB <= (int)sizeof(lds), "every wave has room for 32 rows");
+  if (g.N % (16 / EB) == 0 && (uintptr_t)g.out % 16 == 0) {
+    __syncthreads();  // the last K block has been read
+    uint8_t* const mine = lds + wave * 32 * RB;
+#pragma unroll
+    for (int s = 0; s < SM; s++) {
+#pragma unroll
+      for (int i = 0; i < SN; i++)
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const int byte = (i * 32 + 8 * q + 4 * h) * EB;
+          uint8_t* d = mine + r32 * RB + ((byte / 16) ^ (r32 % 8 % PIECES)) * 16 + byte % 16;
+          const float v[4] = {acc[i][s][4 * q], acc[i][s][4 * q + 1], acc[i][s][4 * q + 2],
+                              acc[i][s][4 * q + 3]};
+          store4<F32>(d, 0, v);
+        }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int u = 0; u < 32 / RPI; u++) {
+        const int row = u * RPI + lane / PIECES, piece = lane % PIECES;
+        const int n = nw + piece * (16 / EB);
+        const int orw = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + row);
+        const u32x4 v =
+            *reinterpret_cast<const u32x4*>(mine + row * RB + (piece ^ (row % 8 % PIECES)) * 16);
+        if (orw >= 0 && n < g.N)
+          *reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(g.out) +
+                                    ((size_t)orw * g.N + n) * EB) = v;
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    return;
+  }
 #pragma unroll
   for (int s = 0; s < SM; s++) {
     if (orow[s] < 0) continue;
@@ -426,17 +468,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
 #pragma unroll
     for (int i = 0; i < SN; i++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int n = nw + i * 32 + 8 * q + 4 * h;
-        const float v[4] = {acc[i][s][4 * q], acc[i][s][4 * q + 1], acc[i][s][4 * q + 2],
-                            acc[i][s][4 * q + 3]};
-        if (wide) {
-          if (n < g.N) store4<F32>(g.out, o + n, v);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; r++)
-            if (n + r < g.N) store1<F32>(g.out, o + n + r, v[r]);
-        }
+      for (int r = 0; r < 16; r++) {
+        const int n = nw + i * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
+        if (n < g.N) store1<F32>(g.out, o + n, acc[i][s][r]);
       }
   }
 }
