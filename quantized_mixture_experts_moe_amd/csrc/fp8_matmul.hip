@@ -19,7 +19,9 @@
 // b feeds the matrix core's row operand and a its
 // column operand, so a lane's results share one row of a (one scale) and are
 // consecutive columns of out.
+#include <stdlib.h>
 #include "block_common.h"
+#include "qmoe_internal.h"
 
 namespace qmoe {
 namespace {
@@ -80,64 +82,150 @@ struct Rows {
   }
 };
 
-// 16 rows x 64 columns per wave, operands straight from memory.
-template <bool GROUPED, bool BBLOCK, bool F32>
-__global__ __launch_bounds__(256) void fp8_matmul_rows16_kernel(Fp8MatmulArgs g) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// ---------------------------------------------------------------------------
+// Few rows: the work is reading b once.  A block computes 16 MS rows x 16 NS
+// columns, its KS waves taking every KS-th K block, so that together they read
+// KS * 128 consecutive bytes of each of b's rows; operands go straight from
+// memory to registers, kRing K blocks ahead, and the waves' sums are added in
+// wave order through LDS.
+constexpr int kRing = 4;
+
+template <int KS, int MS, int NS, bool GROUPED, bool BBLOCK, bool F32>
+__global__ __launch_bounds__(64 * KS) void fp8_matmul_rows_kernel(Fp8MatmulArgs g) {
+  __shared__ f32x4 part[KS][MS * NS][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int l = lane & 15, q = lane >> 4;
-  const int n0 = (blockIdx.x * 4 + wave) * 64;
-  const int m0 = blockIdx.y * 16;
-  if (n0 >= g.N) return;
+  const int n0 = blockIdx.x * 16 * NS;
+  const int m0 = blockIdx.y * 16 * MS;
   const uint8_t* b = g.b;
   const float* bs = g.b_scale;
   if constexpr (GROUPED) {
     if (m0 >= *g.num_padded) return;
     const int e = g.tile_expert[m0 / g.block_m];
-    if (e < 0) return;
     b += (size_t)e * g.N * g.K;
     bs += (size_t)e * ((g.N + 127) / 128) * g.KB;
   }
-  const int orow = Rows<GROUPED>::out_row(g, m0 + l);
-  const int arow = Rows<GROUPED>::a_row(g, orow);
-  const uint8_t* ap = g.a + (size_t)arow * g.K + 16 * q;
-  const uint8_t* bp[4];
+  int arow[MS];
+  const uint8_t* ap[MS];
 #pragma unroll
-  for (int s = 0; s < 4; s++)
+  for (int m = 0; m < MS; m++) {
+    arow[m] = Rows<GROUPED>::a_row(g, Rows<GROUPED>::out_row(g, m0 + 16 * m + l));
+    ap[m] = g.a + (size_t)arow[m] * g.K + 16 * q;
+  }
+  const uint8_t* bp[NS];
+#pragma unroll
+  for (int s = 0; s < NS; s++)
     bp[s] = b + (size_t)min(n0 + 16 * s + l, g.N - 1) * g.K + 16 * q;
-  f32x4 acc[4];
+  const float* sbp = bs + (BBLOCK ? (size_t)(n0 / 128) * g.KB : 0);  // 16 NS divides 128
+
+  struct Step {
+    u32x4 a[MS][2], b[NS][2];
+    float sa[MS], sb;
+  };
+  Step ring[kRing];
+  auto load = [&](Step& st, int kb) {
+    const size_t at = (size_t)kb * 128;
 #pragma unroll
-  for (int s = 0; s < 4; s++) acc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int kb = 0; kb < g.KB; kb++) {
-    const i32x8 av = join(*reinterpret_cast<const u32x4*>(ap + kb * 128),
-                          *reinterpret_cast<const u32x4*>(ap + kb * 128 + 64));
-    const float sa = g.a_scale[(size_t)kb * g.Ma + arow];
+    for (int s = 0; s < NS; s++) {
+      st.b[s][0] = *reinterpret_cast<const u32x4*>(bp[s] + at);
+      st.b[s][1] = *reinterpret_cast<const u32x4*>(bp[s] + at + 64);
+    }
 #pragma unroll
-    for (int s = 0; s < 4; s++) {
-      const i32x8 bv = join(*reinterpret_cast<const u32x4*>(bp[s] + kb * 128),
-                            *reinterpret_cast<const u32x4*>(bp[s] + kb * 128 + 64));
-      const f32x4 t = kblock16<F32>(bv, av);
-      if constexpr (BBLOCK) {
-        const int nb = min(n0 + 16 * s, g.N - 1) / 128;
-        const float sc = sa * bs[(size_t)nb * g.KB + kb];
+    for (int m = 0; m < MS; m++) {
+      st.a[m][0] = *reinterpret_cast<const u32x4*>(ap[m] + at);
+      st.a[m][1] = *reinterpret_cast<const u32x4*>(ap[m] + at + 64);
+      st.sa[m] = g.a_scale[(size_t)kb * g.Ma + arow[m]];
+    }
+    st.sb = BBLOCK ? sbp[kb] : 1.0f;
+  };
+  f32x4 acc[MS][NS];
 #pragma unroll
-        for (int r = 0; r < 4; r++) acc[s][r] = __builtin_fmaf(t[r], sc, acc[s][r]);
-      } else {
+  for (int m = 0; m < MS; m++)
 #pragma unroll
-        for (int r = 0; r < 4; r++) {
-          const int n = min(n0 + 16 * s + 4 * q + r, g.N - 1);
-          acc[s][r] = __builtin_fmaf(t[r] * bs[(size_t)kb * g.N + n], sa, acc[s][r]);
-        }
+    for (int s = 0; s < NS; s++) acc[m][s] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Step& st, int kb) {
+#pragma unroll
+    for (int s = 0; s < NS; s++) {
+      const i32x8 bv = join(st.b[s][0], st.b[s][1]);
+      f32x4 sn = {st.sb, st.sb, st.sb, st.sb};
+      if constexpr (!BBLOCK) {
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+          sn[r] = bs[(size_t)kb * g.N + min(n0 + 16 * s + 4 * q + r, g.N - 1)];
+      }
+#pragma unroll
+      for (int m = 0; m < MS; m++) {
+        const f32x4 t = kblock16<F32>(bv, join(st.a[m][0], st.a[m][1]));
+#pragma unroll
+        for (int r = 0; r < 4; r++)
+          acc[m][s][r] = __builtin_fmaf(t[r], st.sa[m] * sn[r], acc[m][s][r]);
+      }
+    }
+  };
+#pragma unroll
+  for (int u = 0; u < kRing; u++)
+    if (wave + u * KS < g.KB) load(ring[u], wave + u * KS);
+  for (int k0 = wave; k0 < g.KB; k0 += kRing * KS) {
+#pragma unroll
+    for (int u = 0; u < kRing; u++) {
+      const int kb = k0 + u * KS, next = kb + kRing * KS;
+      if (kb < g.KB) {
+        compute(ring[u], kb);
+        if (next < g.KB) load(ring[u], next);
       }
     }
   }
-  if (orow < 0) return;
 #pragma unroll
-  for (int s = 0; s < 4; s++)
+  for (int m = 0; m < MS; m++)
 #pragma unroll
-    for (int r = 0; r < 4; r++) {
-      const int n = n0 + 16 * s + 4 * q + r;
-      if (n < g.N) store1<F32>(g.out, (size_t)orow * g.N + n, acc[s][r]);
+    for (int s = 0; s < NS; s++) part[wave][m * NS + s][lane] = acc[m][s];
+  __syncthreads();
+#pragma unroll
+  for (int j = wave; j < MS * NS; j += KS) {
+    f32x4 v = part[0][j][lane];
+#pragma unroll
+    for (int w = 1; w < KS; w++) {
+      const f32x4 x = part[w][j][lane];
+#pragma unroll
+      for (int r = 0; r < 4; r++) v[r] += x[r];
     }
+    const int orow = Rows<GROUPED>::out_row(g, m0 + 16 * (j / NS) + l);
+    const int n = n0 + 16 * (j % NS) + 4 * q;
+    if (orow < 0) continue;
+    const size_t o = (size_t)orow * g.N + n;
+    if (g.N % 4 == 0 && (uintptr_t)g.out % 16 == 0) {
+      const float w[4] = {v[0], v[1], v[2], v[3]};
+      if (n < g.N) store4<F32>(g.out, o, w);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; r++)
+        if (n + r < g.N) store1<F32>(g.out, o + r, v[r]);
+    }
+  }
+}
+
+template <int MS, bool GROUPED, bool BBLOCK, bool F32>
+hipError_t launch_rows(const Fp8MatmulArgs& g, hipStream_t s) {
+  const int mt = (g.M + 16 * MS - 1) / (16 * MS);
+  if (mt > 65535) return hipErrorInvalidValue;
+  // Two sub-tiles of columns per block where that still gives every CU two
+  // blocks; eight waves where each has a K block to itself.
+  const bool two = (long long)mt * ((g.N + 31) / 32) >= 2 * device_cu_count();
+  const bool eight = g.KB >= 8;
+#define QMOE_CALL(KS, NS)                                                                      \
+  hipLaunchKernelGGL((fp8_matmul_rows_kernel<KS, MS, NS, GROUPED, BBLOCK, F32>),               \
+                     dim3((g.N + 16 * NS - 1) / (16 * NS), mt), dim3(64 * KS), 0, s, g)
+  if (two && eight)
+    QMOE_CALL(8, 2);
+  else if (two)
+    QMOE_CALL(4, 2);
+  else if (eight)
+    QMOE_CALL(8, 1);
+  else
+    QMOE_CALL(4, 1);
+#undef QMOE_CALL
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -170,33 +258,43 @@ __device__ inline float load_f32(Rsrc r, unsigned voff) {
   return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, 0, 0));
 }
 
-// Waits for the wave's copies (vmcnt 0; the barrier alone does not wait for
-// copies to LDS), then for the other waves'.
-__device__ inline void wait_copies() { __builtin_amdgcn_s_waitcnt(0x0F70); }
-__device__ inline void landed() {
-  wait_copies();
-  __syncthreads();
+// Waits until at most N of the wave's memory operations are under way (they
+// end in order; a barrier alone does not wait for copies to LDS).
+template <int N>
+__device__ inline void wait_memory() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
 }
 
-template <int BM_, int BN_, int WM_, int WN_>
+// Barrier of the block that leaves copies to LDS under way (the fence of
+// __syncthreads waits for every one): the wave's own LDS reads and writes are
+// done, and none of the compiler's is moved across.
+__device__ inline void block_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int SM = BM / WM / 32, SN = BN / WN / 32;
   static constexpr int AC = BM / 8 / WAVES, BC = BN / 8 / WAVES;  // copies per wave and K block
+  static constexpr int COPIES = AC + BC + 1;                      // with the scales' one
+  static constexpr int AS = (BM + 63) / 64;                       // waves that copy a's scales
+  // LDS of a stage: a, b, 64 scales per wave.
+  static constexpr int B_AT = BM * 128, S_AT = B_AT + BN * 128, STAGE = S_AT + WAVES * 256;
   static_assert(SM * WM * 32 == BM && SN * WN * 32 == BN, "whole sub-tiles");
   static_assert(AC * WAVES * 8 == BM && BC * WAVES * 8 == BN, "whole copies");
+  static_assert(AS + (BN + 63) / 64 <= WAVES, "one scale copy per wave");
+  static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
 };
 
-template <class C, bool GROUPED, bool BBLOCK, bool F32>
+// OUT32: out is fp32 (the sums of a K split, and fp32 outputs); EXACT: the
+// codes are widened to bf16.  blockIdx.y is the part of a K split.
+template <class C, bool GROUPED, bool BBLOCK, bool EXACT, bool OUT32>
 __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8MatmulArgs g) {
   constexpr int SM = C::SM, SN = C::SN;
-  __shared__ float c0[BBLOCK ? 1 : C::BN], c1[BBLOCK ? 1 : C::BN];  // b's row scales
-  __shared__ __align__(1024) uint8_t lds[2 * (C::BM + C::BN) * 128];
-  uint8_t* const a0 = lds;
-  uint8_t* const b0 = a0 + C::BM * 128;
-  uint8_t* const a1 = b0 + C::BN * 128;
-  uint8_t* const b1 = a1 + C::BM * 128;
+  __shared__ __align__(1024) uint8_t lds[C::STAGES * C::STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
@@ -212,13 +310,15 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   const int band = id / (kBand * ntn), in = id - band * kBand * ntn;
   const int rows = min(kBand, ntm - band * kBand);
   const int m0 = (band * kBand + in % rows) * C::BM, n0 = in / rows * C::BN;
+  const int kb0 = blockIdx.y * g.split_kb, kb1 = min(g.KB, kb0 + g.split_kb);
+  const int NB = (g.N + 127) / 128;
   const uint8_t* b = g.b;
   const float* bs = g.b_scale;
   if constexpr (GROUPED) {
     const int e = g.tile_expert[m0 / g.block_m];
     if (e < 0) return;
     b += (size_t)e * g.N * g.K;
-    bs += (size_t)e * ((g.N + 127) / 128) * g.KB;
+    bs += (size_t)e * NB * g.KB;
   }
   // Copies: 8 lanes per row, the rows of a wave's copy t being 8 t .. 8 t + 7.
   // The chunk order alternates with t, hence two lane offsets where the rows
@@ -230,7 +330,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   const size_t abytes = (GROUPED ? (size_t)g.Ma : (size_t)(g.M - m0)) * K;
   const size_t bbytes = (size_t)(g.N - n0) * K;
   unsigned av[GROUPED ? C::AC : 2];
-  const unsigned bv[2] = {(lane >> 3) * (unsigned)g.K + swz(0), (lane >> 3) * (unsigned)g.K + swz(1)};
+  const unsigned bv[2] = {(lane >> 3) * (unsigned)g.K + swz(0),
+                          (lane >> 3) * (unsigned)g.K + swz(1)};
   if constexpr (GROUPED) {
 #pragma unroll
     for (int i = 0; i < C::AC; i++) {
@@ -242,60 +343,59 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
     av[0] = bv[0];
     av[1] = bv[1];
   }
-  // Scales of the lane's rows, one K block ahead.
-  const int r32 = lane & 31, h = lane >> 5;
-  int orow[SM];
-  unsigned so[SM];
-#pragma unroll
-  for (int s = 0; s < SM; s++) {
-    orow[s] = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + r32);
-    so[s] = 4u * (unsigned)Rows<GROUPED>::a_row(g, orow[s]);
-  }
-  const int nw = n0 + wn * SN * 32;  // the wave's first column
-  const float* sbp = bs + (BBLOCK ? (size_t)(min(nw, g.N - 1) / 128) * g.KB : 0);
-  float sa[SM], nsa[SM], nsb = 1.0f;  // of this K block, of the next one
-  auto take = [&]() {
-#pragma unroll
-    for (int s = 0; s < SM; s++) sa[s] = nsa[s] * nsb;
-  };
-  // (K blocks behind the last one are copies of nothing: empty buffers.)
-  auto load_scales = [&](float* lc, int kb) {
-    const bool any = kb < g.KB;
-    const Rsrc rs = rsrc(g.a_scale + (size_t)kb * g.Ma, any ? (size_t)g.Ma * 4 : 0);
-#pragma unroll
-    for (int s = 0; s < SM; s++) nsa[s] = load_f32(rs, so[s]);
-    if constexpr (BBLOCK) {
-      nsb = load_f32(rsrc(sbp + kb, any ? 4 : 0), 0);
-    } else if (wave < C::BN / 64) {
-      const Rsrc rc = rsrc(bs + (size_t)kb * g.N + n0, any ? (size_t)(g.N - n0) * 4 : 0);
-      copy4(rc, wave * 256 + lane * 4, lc + wave * 64);
+  // The wave's scale copy: 64 rows of a, 64 rows of b, or (lanes 0 and 1) the
+  // tile's two blocks of b; a wave without one copies nothing, so that every
+  // wave has the same number under way.
+  const uint8_t* sbase = reinterpret_cast<const uint8_t*>(bs);
+  size_t sstep = BBLOCK ? 4 : (size_t)g.N * 4, sbytes = 0;
+  unsigned sv = 0;
+  if (wave < C::AS) {
+    sbase = reinterpret_cast<const uint8_t*>(g.a_scale);
+    sstep = sbytes = (size_t)g.Ma * 4;
+    const int slot = m0 + wave * 64 + lane;
+    const bool in_tile = wave * 64 + lane < C::BM;
+    sv = in_tile ? 4u * (unsigned)Rows<GROUPED>::a_row(g, Rows<GROUPED>::out_row(g, slot)) : 0u;
+  } else if constexpr (BBLOCK) {
+    if (wave == C::AS) {
+      sbytes = (size_t)NB * g.KB * 4;
+      sv = 4u * (unsigned)(n0 / 128 + (lane & 1)) * (unsigned)g.KB;
     }
-  };
-  // Copy c of the wave's AC + BC ones of a K block.
-  auto load = [&](uint8_t* la, uint8_t* lb, int kb, int c) {
-    const bool any = kb < g.KB;
+  } else if (wave < C::AS + (C::BN + 63) / 64) {
+    sbytes = (size_t)g.N * 4;
+    sv = 4u * (unsigned)(n0 + (wave - C::AS) * 64 + lane);
+  }
+  // Copy c of the wave's COPIES of K block kb, to stage st.  (K blocks behind
+  // the last one are copies of nothing, from empty buffers.)
+  auto load = [&](uint8_t* st, int kb, int c) {
+    const bool any = kb < kb1;
     if (c < C::AC) {
       const int t = wave * C::AC + c;
       const Rsrc ra = rsrc(abase, any ? abytes : 0);
       if constexpr (GROUPED)
-        copy16(ra, av[c], kb * 128, la + t * 1024);
+        copy16(ra, av[c], kb * 128, st + t * 1024);
       else
         copy16(ra, (C::AC % 2 == 0 ? c : t) % 2 ? av[1] : av[0], t * 8 * g.K + kb * 128,
-               la + t * 1024);
-    } else {
+               st + t * 1024);
+    } else if (c < C::AC + C::BC) {
       const int i = c - C::AC, t = wave * C::BC + i;
       const Rsrc rb = rsrc(bbase, any ? bbytes : 0);
       copy16(rb, (C::BC % 2 == 0 ? i : t) % 2 ? bv[1] : bv[0], t * 8 * g.K + kb * 128,
-             lb + t * 1024);
+             st + C::B_AT + t * 1024);
+    } else {
+      const Rsrc rs = rsrc(sbase + (any ? (size_t)kb * sstep : 0), any ? sbytes : 0);
+      copy4(rs, sv, reinterpret_cast<float*>(st + C::S_AT + wave * 256));
     }
   };
   // Reads: lane's row in a sub-tile and its half of each 64 positions of K.
+  const int r32 = lane & 31, h = lane >> 5;
   int off[2][2];
 #pragma unroll
   for (int j = 0; j < 2; j++)
 #pragma unroll
     for (int e = 0; e < 2; e++)
       off[j][e] = r32 * 128 + 16 * ((4 * j + 2 * h + e) ^ ((r32 >> 1) & 7));
+  const int nw = n0 + wn * SN * 32;  // the wave's first column
+  const int nblk = wn * SN * 32 / 128;
   f32x16 acc[SN][SM];
 #pragma unroll
   for (int i = 0; i < SN; i++)
@@ -308,34 +408,37 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
     return join(*reinterpret_cast<const u32x4*>(t + sub * 4096 + off[j][0]),
                 *reinterpret_cast<const u32x4*>(t + sub * 4096 + off[j][1]));
   };
-  f32x4 sbn[BBLOCK ? 1 : SN][4];  // b's scales of the lane's 16 columns per sub-tile
-  auto row_scales = [&](const float* lc) {
+  // One K block from stage st; the copies of K block kb + STAGES - 1 (to nx)
+  // are issued between the matrix instructions, so that no wave waits in front
+  // of them for the memory pipe to take its copies.
+  auto compute = [&](const uint8_t* st, uint8_t* nx, int kb) {
+    const uint8_t* la = st;
+    const uint8_t* lb = st + C::B_AT;
+    const float* ls = reinterpret_cast<const float*>(st + C::S_AT);
+    const int next = kb + C::STAGES - 1;
+    float sa[SM];
+    const float sb = BBLOCK ? ls[C::AS * 64 + nblk] : 1.0f;
+#pragma unroll
+    for (int s = 0; s < SM; s++) sa[s] = ls[(wm * SM + s) * 32 + r32] * sb;
+    f32x4 sbn[BBLOCK ? 1 : SN][4];  // b's scales of the lane's 16 columns per sub-tile
     if constexpr (!BBLOCK) {
 #pragma unroll
       for (int i = 0; i < SN; i++)
 #pragma unroll
         for (int q = 0; q < 4; q++)
-          sbn[i][q] =
-              *reinterpret_cast<const f32x4*>(lc + (wn * SN + i) * 32 + 8 * q + 4 * h);
+          sbn[i][q] = *reinterpret_cast<const f32x4*>(ls + C::AS * 64 + (wn * SN + i) * 32 +
+                                                      8 * q + 4 * h);
     }
-  };
-  auto scaled = [&](const f32x16& t, int i, int s) {
+    auto scaled = [&](const f32x16& t, int i, int s) {
 #pragma unroll
-    for (int r = 0; r < 16; r++) {
-      if constexpr (BBLOCK)
-        acc[i][s][r] = __builtin_fmaf(t[r], sa[s], acc[i][s][r]);
-      else
-        acc[i][s][r] = __builtin_fmaf(t[r] * sbn[i][r >> 2][r & 3], sa[s], acc[i][s][r]);
-    }
-  };
-  // One K block from LDS; the next one's copies (to na, nb) are issued between
-  // the matrix instructions, so that no wave waits in front of them for the
-  // memory pipe to take its copies.
-  auto compute = [&](const uint8_t* la, const uint8_t* lb, const float* lc, uint8_t* na, uint8_t* nb,
-                     float* nc, int kb) {
-    row_scales(lc);
-    load_scales(nc, kb + 1);
-    if constexpr (F32) {
+      for (int r = 0; r < 16; r++) {
+        if constexpr (BBLOCK)
+          acc[i][s][r] = __builtin_fmaf(t[r], sa[s], acc[i][s][r]);
+        else
+          acc[i][s][r] = __builtin_fmaf(t[r] * sbn[i][r >> 2][r & 3], sa[s], acc[i][s][r]);
+      }
+    };
+    if constexpr (EXACT) {
       // The codes widened to bf16, 16 positions of K per instruction: a lane's
       // chunk of 16 codes feeds two.
       f32x16 t[SN][SM];
@@ -356,8 +459,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
         for (int s = 0; s < SM; s++)
           x[s] = *reinterpret_cast<const u32x4*>(la + (wm * SM + s) * 4096 + o);
 #pragma unroll
-        for (int u = c * (C::AC + C::BC) / 4; u < (c + 1) * (C::AC + C::BC) / 4; u++)
-          load(na, nb, kb + 1, u);
+        for (int u = c * C::COPIES / 4; u < (c + 1) * C::COPIES / 4; u++) load(nx, next, u);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
           bf16x8 xs[SM];
@@ -399,8 +501,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
           t[q & 1] = z;
           constexpr int kParts = (SM * SN + 1) / 2;  // all copies by the middle of the step
 #pragma unroll
-          for (int u = 0; u < C::AC + C::BC; u++)
-            if (u * kParts / (C::AC + C::BC) == q) load(na, nb, kb + 1, u);
+          for (int u = 0; u < C::COPIES; u++)
+            if (u * kParts / C::COPIES == q) load(nx, next, u);
           // The scaling of the sub-tile before runs while the matrix core works.
           if (q > 0) scaled(t[(q - 1) & 1], (q - 1) % SN, (q - 1) / SN);
         }
@@ -408,29 +510,43 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
       scaled(t[(SM * SN - 1) & 1], SN - 1, SM - 1);
     }
   };
-  load_scales(c0, 0);
 #pragma unroll
-  for (int u = 0; u < C::AC + C::BC; u++) load(a0, b0, 0, u);
-  for (int kb = 0; kb < g.KB; kb += 2) {
-    landed();  // stage 0 is there, stage 1 is free
-    take();
-    compute(a0, b0, c0, a1, b1, c1, kb);
-    if (kb + 1 >= g.KB) break;
-    landed();
-    take();
-    compute(a1, b1, c1, a0, b0, c0, kb + 1);
+  for (int s = 0; s < C::STAGES - 1; s++)
+#pragma unroll
+    for (int u = 0; u < C::COPIES; u++) load(lds + s * C::STAGE, kb0 + s, u);
+  for (int kb = kb0;;) {
+    bool done = false;
+#pragma unroll
+    for (int s = 0; s < C::STAGES; s++) {
+      if (done) continue;
+      // Stage s has landed (the stages behind it may be under way), in every
+      // wave; and every wave is done with the stage before, which is free now.
+      wait_memory<(C::STAGES - 2) * C::COPIES>();
+      block_barrier();
+      compute(lds + s * C::STAGE, lds + (s + C::STAGES - 1) % C::STAGES * C::STAGE, kb);
+      done = ++kb >= kb1;
+    }
+    if (done) break;
   }
-  wait_copies();  // no copy outlives the block's LDS
+  wait_memory<0>();  // no copy is under way when LDS is used again, or ends
+
   // A lane holds four times four consecutive columns of its row per sub-tile.
   // Where rows can be stored in 16-byte pieces, each wave turns its tile over
   // in LDS, 32 rows at a time, so that consecutive lanes store consecutive
   // bytes (the pieces of a row in the order p ^ row % 8, against bank
   // conflicts).
-  constexpr int EB = F32 ? 4 : 2;             // bytes per value
+  uint8_t* const out = reinterpret_cast<uint8_t*>(g.out) + (size_t)blockIdx.y * g.M * g.N * 4;
+  constexpr int EB = OUT32 ? 4 : 2;           // bytes per value
   constexpr int RB = SN * 32 * EB;            // bytes per row of the wave's tile
   constexpr int PIECES = RB / 16, RPI = 64 / PIECES;  // pieces per row, rows per store
   static_assert(C::WAVES * 32 * RB <= (int)sizeof(lds), "every wave has room for 32 rows");
-  if (g.N % (16 / EB) == 0 && (uintptr_t)g.out % 16 == 0) {
+  if (g.N % (16 / EB) == 0 && (uintptr_t)out % 16 == 0) {
+    int orow[SM][32 / RPI];  // before the stores: a load behind them would wait for them
+#pragma unroll
+    for (int s = 0; s < SM; s++)
+#pragma unroll
+      for (int u = 0; u < 32 / RPI; u++)
+        orow[s][u] = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + u * RPI + lane / PIECES);
     __syncthreads();  // the last K block has been read
     uint8_t* const mine = lds + wave * 32 * RB;
 #pragma unroll
@@ -443,19 +559,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
           uint8_t* d = mine + r32 * RB + ((byte / 16) ^ (r32 % 8 % PIECES)) * 16 + byte % 16;
           const float v[4] = {acc[i][s][4 * q], acc[i][s][4 * q + 1], acc[i][s][4 * q + 2],
                               acc[i][s][4 * q + 3]};
-          store4<F32>(d, 0, v);
+          store4<OUT32>(d, 0, v);
         }
       __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int u = 0; u < 32 / RPI; u++) {
         const int row = u * RPI + lane / PIECES, piece = lane % PIECES;
         const int n = nw + piece * (16 / EB);
-        const int orw = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + row);
         const u32x4 v =
             *reinterpret_cast<const u32x4*>(mine + row * RB + (piece ^ (row % 8 % PIECES)) * 16);
-        if (orw >= 0 && n < g.N)
-          *reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(g.out) +
-                                    ((size_t)orw * g.N + n) * EB) = v;
+        if (orow[s][u] >= 0 && n < g.N)
+          *reinterpret_cast<u32x4*>(out + ((size_t)orow[s][u] * g.N + n) * EB) = v;
       }
       __builtin_amdgcn_wave_barrier();
     }
@@ -463,73 +577,142 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   }
 #pragma unroll
   for (int s = 0; s < SM; s++) {
-    if (orow[s] < 0) continue;
-    const size_t o = (size_t)orow[s] * g.N;
+    const int orow = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + r32);
+    if (orow < 0) continue;
+    const size_t o = (size_t)orow * g.N;
 #pragma unroll
     for (int i = 0; i < SN; i++)
 #pragma unroll
       for (int r = 0; r < 16; r++) {
         const int n = nw + i * 32 + 8 * (r >> 2) + 4 * h + (r & 3);
-        if (n < g.N) store1<F32>(g.out, o + n, acc[i][s][r]);
+        if (n < g.N) store1<OUT32>(out, o + n, acc[i][s][r]);
       }
   }
 }
 
-template <class C, bool GROUPED, bool BBLOCK, bool F32>
-hipError_t launch_tile(const Fp8MatmulArgs& g, hipStream_t s) {
+// out = the sum of the parts of a K split, in order.
+template <bool F32>
+__global__ __launch_bounds__(256) void fp8_matmul_sum_kernel(const float* __restrict__ parts,
+                                                             int splits, size_t count, void* out,
+                                                             bool wide) {
+  const size_t i = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= count) return;
+  if (wide) {  // count is a multiple of 4, out is aligned for 4 values
+    f32x4 v = *reinterpret_cast<const f32x4*>(parts + i);
+    for (int p = 1; p < splits; p++) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(parts + p * count + i);
+#pragma unroll
+      for (int r = 0; r < 4; r++) v[r] += x[r];
+    }
+    const float w[4] = {v[0], v[1], v[2], v[3]};
+    store4<F32>(out, i, w);
+  } else {
+    for (size_t j = i; j < i + 4 && j < count; j++) {
+      float v = parts[j];
+      for (int p = 1; p < splits; p++) v += parts[p * count + j];
+      store1<F32>(out, j, v);
+    }
+  }
+}
+
+template <class C, bool GROUPED, bool BBLOCK, bool EXACT>
+hipError_t launch_tile(Fp8MatmulArgs g, int splits, hipStream_t s) {
   const long long total =
       (long long)((g.N + C::BN - 1) / C::BN) * ((g.M + C::BM - 1) / C::BM);
   if (total > (1ll << 30)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, F32>),
-                     dim3((unsigned)((total + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
+  const dim3 grid((unsigned)((total + 7) / 8 * 8), splits), block(C::THREADS);
+  g.split_kb = (g.KB + splits - 1) / splits;
+  if constexpr (!GROUPED) {
+    if (splits > 1) {
+      void* out = g.out;
+      g.out = g.parts;
+      hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, false, BBLOCK, EXACT, true>), grid, block, 0,
+                         s, g);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+      const size_t count = (size_t)g.M * g.N;
+      const bool wide = count % 4 == 0 && (uintptr_t)out % 16 == 0;
+      const dim3 sg((unsigned)((count + 1023) / 1024));
+      if (g.out_f32)
+        hipLaunchKernelGGL(fp8_matmul_sum_kernel<true>, sg, dim3(256), 0, s, g.parts, splits,
+                           count, out, wide);
+      else
+        hipLaunchKernelGGL(fp8_matmul_sum_kernel<false>, sg, dim3(256), 0, s, g.parts, splits,
+                           count, out, wide);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, EXACT, EXACT>), grid, block, 0, s,
+                     g);
   return hipGetLastError();
+}
+
+typedef Tile<256, 256, 2, 4, 2> Big;
+typedef Tile<128, 128, 2, 2, 2> Mid;
+typedef Tile<64, 64, 2, 2, 4> Small;
+
+// Tile (0 few rows, 1 small, 2 middle, 3 big) and parts of K of a dense product.
+struct Plan {
+  int tile, splits;
+};
+Plan plan(int M, int N, int K, bool big) {
+  const int force = getenv("QT") ? atoi(getenv("QT")) : -1, fs = getenv("QS") ? atoi(getenv("QS")) : 1;
+  if (force >= 0) return {force, fs};
+  if (M <= 32) return {0, 1};
+  if (big && (long long)((M + 255) / 256) * ((N + 255) / 256) >= 200) return {3, 1};
+  return {2, 1};
 }
 
 }  // namespace
 
-size_t fp8_matmul_parts_bytes(int, int, int) { return 0; }
-
-// Rows up to which the untiled kernel is taken.
-constexpr int kFewRows = 32;
-
-hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
-  typedef Tile<128, 128, 2, 2> Mid;
-  typedef Tile<256, 256, 2, 4> Big;
-  if (g.M >= kFewRows) {
-    if (g.out_f32)
-      return g.b_block ? launch_tile<Mid, false, true, true>(g, s)
-                       : launch_tile<Mid, false, false, true>(g, s);
-    if (!g.b_block) return launch_tile<Mid, false, false, false>(g, s);
-    const long long big = (long long)((g.M + 255) / 256) * ((g.N + 255) / 256);
-    return big >= 200 ? launch_tile<Big, false, true, false>(g, s)
-                      : launch_tile<Mid, false, true, false>(g, s);
-  }
-  const dim3 grid((g.N + 255) / 256, (g.M + 15) / 16), block(256);
-#define QMOE_CALL(BB, F32) \
-  hipLaunchKernelGGL((fp8_matmul_rows16_kernel<false, BB, F32>), grid, block, 0, s, g)
-  if (g.b_block && g.out_f32)
-    QMOE_CALL(true, true);
-  else if (g.b_block)
-    QMOE_CALL(true, false);
-  else if (g.out_f32)
-    QMOE_CALL(false, true);
-  else
-    QMOE_CALL(false, false);
-#undef QMOE_CALL
-  return hipGetLastError();
+size_t fp8_matmul_parts_bytes(int M, int N, int K) {
+  const int a = plan(M, N, K, true).splits, b = plan(M, N, K, false).splits;
+  const int most = a > b ? a : b;
+  return most > 1 ? (size_t)most * M * N * 4 : 0;
 }
 
 namespace {
-template <bool F32>
+template <bool BBLOCK, bool EXACT>
+hipError_t dense(const Fp8MatmulArgs& g, hipStream_t s) {
+  const Plan p = plan(g.M, g.N, g.K, BBLOCK && !EXACT);
+  if (p.tile == 0) {
+    return g.M <= 16 ? launch_rows<1, false, BBLOCK, EXACT>(g, s)
+                     : launch_rows<2, false, BBLOCK, EXACT>(g, s);
+  }
+  if constexpr (BBLOCK && !EXACT) {
+    if (p.tile == 3) return launch_tile<Big, false, true, false>(g, p.splits, s);
+  }
+  if (p.tile == 1) return launch_tile<Small, false, BBLOCK, EXACT>(g, p.splits, s);
+  if constexpr (!EXACT) if (p.tile == 4) return launch_tile<Tile<128,256,2,4,3>, false, BBLOCK, EXACT>(g, p.splits, s);
+  if constexpr (!EXACT) if (p.tile == 5) return launch_tile<Tile<256,128,4,2,3>, false, BBLOCK, EXACT>(g, p.splits, s);
+  if (p.tile == 6) return launch_tile<Tile<64,128,2,2,3>, false, BBLOCK, EXACT>(g, p.splits, s);
+  if (getenv("QM")) return launch_tile<Tile<128,128,2,2,4>, false, BBLOCK, EXACT>(g, p.splits, s);
+  return launch_tile<Mid, false, BBLOCK, EXACT>(g, p.splits, s);
+}
+
+template <bool EXACT>
 hipError_t grouped(const Fp8MatmulArgs& g, hipStream_t s) {
-  if (g.block_m == 128) return launch_tile<Tile<128, 128, 2, 2>, true, true, F32>(g, s);
-  if (g.block_m == 64) return launch_tile<Tile<64, 128, 1, 4>, true, true, F32>(g, s);
-  if (g.block_m == 32) return launch_tile<Tile<32, 128, 1, 4>, true, true, F32>(g, s);
-  const dim3 grid((g.N + 255) / 256, (g.M + 15) / 16), block(256);
-  hipLaunchKernelGGL((fp8_matmul_rows16_kernel<true, true, F32>), grid, block, 0, s, g);
-  return hipGetLastError();
+  const char*q=getenv("QG");
+  if (g.block_m == 128) {
+  if(q&&q[0]=='1') return launch_tile<Tile<128,128,2,2,4>, true, true, EXACT>(g, 1, s);
+  if(q&&q[0]=='2') return launch_tile<Tile<128,128,2,2,3>, true, true, EXACT>(g, 1, s);
+  if constexpr(!EXACT) if(q&&q[0]=='3') return launch_tile<Tile<128,256,2,4,3>, true, true, EXACT>(g, 1, s);
+  return launch_tile<Mid, true, true, EXACT>(g, 1, s);
+  }
+  if (g.block_m == 64) return launch_tile<Tile<64, 128, 1, 4, 3>, true, true, EXACT>(g, 1, s);
+  if (g.block_m == 32) {
+  if(q&&q[0]=='1') return launch_tile<Tile<32, 128, 1, 4, 2>, true, true, EXACT>(g, 1, s);
+  if(q&&q[0]=='2') return launch_tile<Tile<32, 128, 1, 4, 4>, true, true, EXACT>(g, 1, s);
+  return launch_tile<Tile<32, 128, 1, 4, 3>, true, true, EXACT>(g, 1, s);
+  }
+  return launch_rows<1, true, true, EXACT>(g, s);
 }
 }  // namespace
+
+hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
+  if (g.b_block) return g.out_f32 ? dense<true, true>(g, s) : dense<true, false>(g, s);
+  return g.out_f32 ? dense<false, true>(g, s) : dense<false, false>(g, s);
+}
 
 hipError_t launch_fp8_grouped_matmul(const Fp8MatmulArgs& g, hipStream_t s) {
   return g.out_f32 ? grouped<true>(g, s) : grouped<false>(g, s);

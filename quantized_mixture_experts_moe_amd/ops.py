@@ -469,38 +469,72 @@ def decode_forward(scheme: str, logits: torch.Tensor, x: torch.Tensor,
 # shapes, types and devices here (ValueError), since the C ABI sees pointers
 # only, and run on the current stream of the tensors' device.
 
-def _need(ok: bool, what: str):
+# These checks and look-ups stand in front of calls whose kernels take a few
+# microseconds, so messages are formed only when they are raised.
+
+def _need(ok, what: str, *values):
     if not ok:
-        raise ValueError(what)
+        raise ValueError(what % values if values else what)
 
 
-def _tensor(t, name: str, shape, *dtypes):
-    _need(isinstance(t, torch.Tensor), f"{name} must be a tensor")
-    _need(tuple(t.shape) == tuple(shape), f"{name} must have shape {tuple(shape)}, not "
-                                          f"{tuple(t.shape)}")
-    _need(t.dtype in dtypes, f"{name} must be {' or '.join(str(d) for d in dtypes)}, not "
-                             f"{t.dtype}")
+def _tensor(t, name: str, shape: tuple, *dtypes):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, not {t.dtype}")
 
 
-def _one_device(*ts):
+def _one_device(first, *others):
     """The device of the tensors given (None for one left out)."""
-    devs = {t.device for t in ts if t is not None}
-    _need(len(devs) == 1 and next(iter(devs)).type == "cuda",
-          f"all tensors must live on one GPU, not on {sorted(map(str, devs))}")
-    return next(iter(devs))
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"tensors passed to libqmoe must live on the GPU, not on {dev}")
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must live on one GPU, not on {dev} and {t.device}")
+    return dev
+
+
+def _addr(t):
+    """A tensor's address (None for one left out)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libqmoe must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(dev) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# The same look-up without a Stream object (0.1 against 1.9 us), where this
+# torch has it.
+_raw_stream_by_index = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(dev, name: str, *args):
     """The library call `name` with the device current (a launch goes to the
     current device's context) and its current stream as the last argument."""
-    with torch.cuda.device(dev):
-        _check(getattr(_lib(), name)(*args, _stream(dev)), name)
+    fn = getattr(_lib(), name)
+    stream = _raw_stream(dev) if _raw_stream_by_index is None else _raw_stream_by_index(dev.index)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != QMOE_OK:
+        raise QmoeError(status, name)
 
 
 def _float_kind(t, name: str) -> int:
-    _need(t.dtype in (torch.bfloat16, torch.float32), f"{name} must be bfloat16 or float32, not "
-                                                      f"{t.dtype}")
-    return QMOE_DT_F32 if t.dtype == torch.float32 else QMOE_DT_BF16
+    if t.dtype == torch.bfloat16:
+        return QMOE_DT_BF16
+    if t.dtype == torch.float32:
+        return QMOE_DT_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, not {t.dtype}")
 
 
 def _blocks(n: int) -> int:
@@ -513,7 +547,7 @@ def fp8_quant(x: torch.Tensor, block: bool = False, act: Optional[str] = None, r
     [E, N, K]; act="silu_mul": [M, 2K] = gate | up).  Returns "codes" (uint8
     e4m3) and "scale" with `rows`, "codes_t" and "scale_t" (the transpose,
     groups along the columns of x) with `cols`."""
-    _need(act in (None, "silu_mul"), f"act must be None or 'silu_mul', not {act!r}")
+    _need(act in (None, "silu_mul"), "act must be None or 'silu_mul', not %r", act)
     _need(rows or cols, "rows or cols (or both)")
     _need(not (block and act), "block scales are for weights: act does not go with them")
     _need(x.dim() == 2 or (block and x.dim() == 3), "x must be [M, K] (or [E, N, K] with block)")
@@ -538,17 +572,17 @@ def fp8_quant(x: torch.Tensor, block: bool = False, act: Optional[str] = None, r
         out["codes_t"] = new(lead + (K, 128 * _blocks(M)), torch.uint8)
         out["scale_t"] = new(lead + ((_blocks(K), _blocks(M)) if block else (_blocks(M), K)),
                              torch.float32)
-    _call(dev, "qmoe_fp8_quant", _ptr(x), dt, B, M, K, int(block), int(act is not None),
-          _ptr(out.get("codes")), _ptr(out.get("scale")), _ptr(out.get("codes_t")),
-          _ptr(out.get("scale_t")))
+    _call(dev, "qmoe_fp8_quant", _addr(x), dt, B, M, K, int(block), int(act is not None),
+          _addr(out.get("codes")), _addr(out.get("scale")), _addr(out.get("codes_t")),
+          _addr(out.get("scale_t")))
     return out
 
 
 def _operand(codes, scale, name: str, block: bool, lead=()):
     """Checks codes [.., rows, K] with their scales; returns (rows, K)."""
-    _need(codes.dim() == 2 + len(lead), f"{name} must have {2 + len(lead)} axes")
+    _need(codes.dim() == 2 + len(lead), "%s must have %d axes", name, 2 + len(lead))
     n, k = codes.shape[-2:]
-    _need(k >= 128 and k % 128 == 0, f"{name}'s row length {k} is not a multiple of 128")
+    _need(k >= 128 and k % 128 == 0, "%s's row length %d is not a multiple of 128", name, k)
     _tensor(codes, name, lead + (n, k), torch.uint8)
     _tensor(scale, f"{name}_scale", lead + ((_blocks(n), k // 128) if block else (k // 128, n)),
             torch.float32)
@@ -573,15 +607,15 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     b_block says that b's scales are per 128 x 128 block, not per row."""
     M, K = _operand(a, a_scale, "a", False)
     N, K2 = _operand(b, b_scale, "b", b_block)
-    _need(K == K2, f"a's rows have {K} values, b's {K2}")
+    _need(K == K2, "a's rows have %d values, b's %d", K, K2)
     _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
     dev = _one_device(a, a_scale, b, b_scale, ws, out)
     out = _out(out, (M, N), out_dtype, dev)
     need = fp8_matmul_workspace(M, N, K)
     if ws is None or ws.numel() * ws.element_size() < need:
         ws = _ws(need, dev) if need else None
-    _call(dev, "qmoe_fp8_matmul", _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), int(b_block), M,
-          N, K, _ptr(out), _float_kind(out, "out"), _ptr(ws),
+    _call(dev, "qmoe_fp8_matmul", _addr(a), _addr(a_scale), _addr(b), _addr(b_scale), int(b_block), M,
+          N, K, _addr(out), _float_kind(out, "out"), _addr(ws),
           0 if ws is None else ws.numel() * ws.element_size())
     return out
 
@@ -597,22 +631,22 @@ def fp8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
     E = b.shape[0]
     rows, K = _operand(a, a_scale, "a", False)
     N, K2 = _operand(b, b_scale, "b", True, (E,))
-    _need(K == K2, f"a's rows have {K} values, b's {K2}")
-    _need(k >= 1 and (not pair_rows or rows % k == 0), f"{rows} pair rows are not a multiple of "
-                                                        f"k = {k}")
+    _need(K == K2, "a's rows have %d values, b's %d", K, K2)
+    _need(k >= 1 and (not pair_rows or rows % k == 0),
+          "%d pair rows are not a multiple of k = %d", rows, k)
     _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
     T, bm = rows // k if pair_rows else rows, al["block_m"]
     cap = align_capacity(T, k, E, bm)
-    _need(cap > 0, f"bad sizes: T {T}, k {k}, E {E}, block_m {bm}")
+    _need(cap > 0, "bad sizes: T %d, k %d, E %d, block_m %d", T, k, E, bm)
     _tensor(al["sorted_pair_ids"], "sorted_pair_ids", (cap,), torch.int32)
     _tensor(al["tile_expert"], "tile_expert", (cap // bm,), torch.int32)
     _tensor(al["num_padded"], "num_padded", (1,), torch.int32)
     dev = _one_device(a, a_scale, b, b_scale, al["sorted_pair_ids"], al["tile_expert"],
                       al["num_padded"], out)
     out = _out(out, (T * k, N), out_dtype, dev)
-    _call(dev, "qmoe_fp8_grouped_matmul", _ptr(a), _ptr(a_scale), int(pair_rows), _ptr(b),
-          _ptr(b_scale), _ptr(al["sorted_pair_ids"]), _ptr(al["tile_expert"]),
-          _ptr(al["num_padded"]), T, k, E, bm, N, K, _ptr(out), _float_kind(out, "out"))
+    _call(dev, "qmoe_fp8_grouped_matmul", _addr(a), _addr(a_scale), int(pair_rows), _addr(b),
+          _addr(b_scale), _addr(al["sorted_pair_ids"]), _addr(al["tile_expert"]),
+          _addr(al["num_padded"]), T, k, E, bm, N, K, _addr(out), _float_kind(out, "out"))
     return out
 
 
@@ -631,7 +665,7 @@ def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor
     w13 [E, 2I, H], w2 [E, H, I] codes and their 128 x 128 block scales
     (fp8_quant(w, block=True)), H % 128 == 0, I % 128 == 0."""
     T, E = logits.shape
-    _need(x.shape[0] == T, f"x has {x.shape[0]} rows, logits {T}")
+    _need(x.shape[0] == T, "x has %d rows, logits %d", x.shape[0], T)
     block_m = fp8_block_m(T, k, E)
     with torch.cuda.device(_one_device(logits, x)):
         ids, w, al = route_align(logits, k, block_m)
@@ -647,7 +681,7 @@ def _mask_ptr(mask, T: int):
     if mask is None:
         return None
     _tensor(mask, "mask", (T,), torch.uint8, torch.bool)
-    return _ptr(mask)
+    return _addr(mask)
 
 
 def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
@@ -669,8 +703,8 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
          "counts": torch.empty(E, dtype=torch.int32, device=dev),
          "probs": torch.empty(E, dtype=torch.float32, device=dev),
          "tokens": torch.empty(1, dtype=torch.int32, device=dev)}
-    _call(dev, "qmoe_balance", _ptr(logits), _ptr(topk_ids), _mask_ptr(mask, T), T, E, k, coef,
-          _ptr(r["loss"]), _ptr(r["counts"]), _ptr(r["probs"]), _ptr(r["tokens"]), _ptr(ws),
+    _call(dev, "qmoe_balance", _addr(logits), _addr(topk_ids), _mask_ptr(mask, T), T, E, k, coef,
+          _addr(r["loss"]), _addr(r["counts"]), _addr(r["probs"]), _addr(r["tokens"]), _addr(ws),
           ws.numel() * ws.element_size())
     return r
 
@@ -688,14 +722,15 @@ def balance_loss_backward(logits: torch.Tensor, counts: torch.Tensor, tokens: to
     _tensor(dloss, "dloss", (1,), torch.float32)
     dev = _one_device(logits, counts, tokens, dloss, mask, out)
     out = _out(out, (T, E), torch.float32, dev)
-    _call(dev, "qmoe_balance_backward", _ptr(logits), _mask_ptr(mask, T), _ptr(counts),
-          _ptr(tokens), _ptr(dloss), T, E, k, coef, _ptr(out))
+    _call(dev, "qmoe_balance_backward", _addr(logits), _mask_ptr(mask, T), _addr(counts),
+          _addr(tokens), _addr(dloss), T, E, k, coef, _addr(out))
     return out
 
 
 def _new_form(form: str, T: int, H: int, dev):
     """Code of a form and its new (n, scale)."""
-    _need(form in NORM_FORMS, f"a norm is written as one of {sorted(NORM_FORMS)}, not {form!r}")
+    _need(form in NORM_FORMS,
+          "a norm is written as one of %s, not %r", list(NORM_FORMS), form)
     if form in ("bf16", "f32"):
         dt = torch.bfloat16 if form == "bf16" else torch.float32
         return NORM_FORMS[form], torch.empty((T, H), dtype=dt, device=dev), None
@@ -714,12 +749,12 @@ def _gate_kind(gate, T: int, H: int, dtype):
         return 0, None
     if gate.dim() == 1:
         _tensor(gate, "a gate per column", (H,), torch.float32)
-        return 1, _ptr(gate)
+        return 1, _addr(gate)
     if tuple(gate.shape) == (T, 1) and (H > 1 or gate.dtype != dtype):
         _tensor(gate, "a gate per token", (T, 1), torch.float32)
-        return 2, _ptr(gate)
+        return 2, _addr(gate)
     _tensor(gate, "gate", (T, H), dtype)
-    return 3, _ptr(gate)
+    return 3, _addr(gate)
 
 
 def pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, out: str = "bf16"):
@@ -732,7 +767,7 @@ def pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, out: str 
     _tensor(weight, "weight", (H,), torch.float32)
     dev = _one_device(x, weight)
     form, n, scale = _new_form(out, T, H, dev)
-    _call(dev, "qmoe_pre_norm", _ptr(x), dt, _ptr(weight), eps, T, H, form, _ptr(n), _ptr(scale))
+    _call(dev, "qmoe_pre_norm", _addr(x), dt, _addr(weight), eps, T, H, form, _addr(n), _addr(scale))
     return n, scale
 
 
@@ -756,8 +791,8 @@ def post_norm(y: torch.Tensor, weight: torch.Tensor, x: torch.Tensor,
     if next_weight is not None:
         _tensor(next_weight, "next_weight", (H,), torch.float32)
         form, n, scale = _new_form(next_out, T, H, dev)
-    _call(dev, "qmoe_post_norm", _ptr(y), _ptr(x), dt, _ptr(weight), gp, kind, alpha, eps, T, H,
-          _ptr(out), _ptr(next_weight), form, _ptr(n), _ptr(scale))
+    _call(dev, "qmoe_post_norm", _addr(y), _addr(x), dt, _addr(weight), gp, kind, alpha, eps, T, H,
+          _addr(out), _addr(next_weight), form, _addr(n), _addr(scale))
     return out, n, scale
 
 
@@ -784,8 +819,8 @@ def pre_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, e
     dx = torch.empty_like(x)
     dw = torch.empty(H, dtype=torch.float32, device=dev)
     ws, nbytes = _norm_ws(ws, H, dev)
-    _call(dev, "qmoe_pre_norm_backward", _ptr(dn), _ptr(x), dt, _ptr(weight), eps, _ptr(dres), T,
-          H, _ptr(dx), _ptr(dw), _ptr(ws), nbytes)
+    _call(dev, "qmoe_pre_norm_backward", _addr(dn), _addr(x), dt, _addr(weight), eps, _addr(dres), T,
+          H, _addr(dx), _addr(dw), _addr(ws), nbytes)
     return dx, dw
 
 
@@ -806,7 +841,7 @@ def post_norm_backward(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor
          "dw": torch.empty(H, dtype=torch.float32, device=dev),
          "dgate": None if gate is None else torch.empty_like(gate)}
     ws, nbytes = _norm_ws(ws, H, dev)
-    _call(dev, "qmoe_post_norm_backward", _ptr(dout), _ptr(y), dt, _ptr(weight), gp, kind, alpha,
-          eps, T, H, _ptr(r["dy"]), _ptr(r["dres"]), _ptr(r["dw"]), _ptr(r["dgate"]), _ptr(ws),
+    _call(dev, "qmoe_post_norm_backward", _addr(dout), _addr(y), dt, _addr(weight), gp, kind, alpha,
+          eps, T, H, _addr(r["dy"]), _addr(r["dres"]), _addr(r["dw"]), _addr(r["dgate"]), _addr(ws),
           nbytes)
     return r

@@ -180,7 +180,7 @@ MATMUL = [(1, 1, 128), (1, 2048, 2048), (2, 130, 256), (5, 63, 384), (15, 16, 12
           (17, 513, 640), (31, 33, 128), (33, 255, 256), (48, 1000, 384), (64, 256, 1024),
           (65, 129, 2304), (100, 384, 4096), (128, 128, 128), (129, 257, 384), (200, 200, 2048),
           (256, 256, 256), (300, 500, 640), (511, 777, 512), (640, 1024, 256), (1000, 129, 4224),
-          (2048, 300, 128), (2000, 2100, 384), (4100, 512, 256), (3, 8192, 128), (8, 16, 8192)]
+          (2048, 300, 128), (2000, 2100, 384), (4100, 512, 256), (3700, 3650, 384), (3, 8192, 128), (8, 16, 8192)]
 
 
 @pytest.mark.parametrize("b_block", [True, False])
