@@ -404,17 +404,17 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
  *    pair_rows = 1: [T*k, K], row(p) = p (the second one); a_scale
  *    [K/128, rows of a].
  * b [E, N, K] with b_scale [E, ceil(N/128), K/128].
- * sorted_pair_ids, tile_expert, num_padded: qmoe_align's outputs for the
- *   same T, k, E and block_m.  out [T*k, N] bf16 or fp32; rows of pairs that
+ * sorted_pair_ids, tile_expert, expert_offsets, num_padded: qmoe_align's
+ *   outputs for the same T, k, E and block_m.  out [T*k, N] bf16 or fp32; rows of pairs that
  *   qmoe_align dropped are left as they are.
- * K % 128 == 0, any N; E <= 1024, a below 4 GiB, N <= 2^24, K <= 2^22
+ * K % 128 == 0, any N; E <= 1024, a up to 3 GiB, N <= 2^24, K <= 2^22
  * (QMOE_ERR_UNSUPPORTED).                                                 */
 qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int32_t pair_rows,
                                     const uint8_t* b, const float* b_scale,
                                     const int32_t* sorted_pair_ids, const int32_t* tile_expert,
-                                    const int32_t* num_padded, int32_t T, int32_t k, int32_t E,
-                                    int32_t block_m, int32_t N, int32_t K, void* out,
-                                    int32_t out_dtype, void* stream);
+                                    const int32_t* expert_offsets, const int32_t* num_padded,
+                                    int32_t T, int32_t k, int32_t E, int32_t block_m, int32_t N,
+                                    int32_t K, void* out, int32_t out_dtype, void* stream);
 
 /* ---------------------------------------------------------------------
  * qmoe_balance -- the router's balance loss and per-expert counts.  With p

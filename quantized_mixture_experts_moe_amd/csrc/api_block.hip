@@ -113,7 +113,8 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
 qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int32_t pair_rows,
                                     const uint8_t* b, const float* b_scale,
                                     const int32_t* sorted_pair_ids, const int32_t* tile_expert,
-                                    const int32_t* num_padded, int32_t T, int32_t k, int32_t E,
+                                    const int32_t* expert_offsets, const int32_t* num_padded,
+                                    int32_t T, int32_t k, int32_t E,
                                     int32_t block_m, int32_t N, int32_t K, void* out,
                                     int32_t out_dtype, void* stream) {
   if (T < 0 || k < 1 || E < 1 || k > E || N < 1 || K < 128 || K % 128 != 0 || pair_rows < 0 ||
@@ -123,10 +124,12 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
     return QMOE_ERR_INVALID_ARG;
   if ((long long)T * k > (1ll << 30)) return QMOE_ERR_INVALID_ARG;
   if (E > 1024 || N > (1 << 24) || K > kMaxK) return QMOE_ERR_UNSUPPORTED;
-  // Gathered rows are addressed with 32-bit byte offsets.
-  if ((uint64_t)T * (pair_rows ? k : 1) * K >= (1ull << 32)) return QMOE_ERR_UNSUPPORTED;
+  // Gathered rows are addressed with 32-bit byte offsets below 3 GiB (the
+  // kernel's offset of no row).
+  if ((uint64_t)T * (pair_rows ? k : 1) * K > (3ull << 30)) return QMOE_ERR_UNSUPPORTED;
   if (T == 0) return QMOE_OK;
-  if (!a || !a_scale || !b || !b_scale || !sorted_pair_ids || !tile_expert || !num_padded || !out)
+  if (!a || !a_scale || !b || !b_scale || !sorted_pair_ids || !tile_expert || !expert_offsets ||
+      !num_padded || !out)
     return QMOE_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scale, 4) || !aligned(b_scale, 4) ||
       !aligned(out, elem(out_dtype)))
@@ -146,6 +149,7 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
   g.out_f32 = out_dtype == QMOE_DT_F32;
   g.sorted = sorted_pair_ids;
   g.tile_expert = tile_expert;
+  g.expert_offsets = expert_offsets;
   g.num_padded = num_padded;
   g.P = T * k;
   g.k = k;

@@ -36,6 +36,7 @@ struct Fp8MatmulArgs {
   // grouped
   const int32_t* sorted;
   const int32_t* tile_expert;
+  const int32_t* expert_offsets;
   const int32_t* num_padded;
   int P, k, block_m, E;
   bool pair_rows;

@@ -19,7 +19,6 @@
 // b feeds the matrix core's row operand and a its
 // column operand, so a lane's results share one row of a (one scale) and are
 // consecutive columns of out.
-#include <stdlib.h>
 #include "block_common.h"
 #include "qmoe_internal.h"
 
@@ -30,6 +29,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+constexpr unsigned kNowhere = 0xC0000000u;  // an offset behind every buffer of gathered rows
 constexpr int kUnit = 127;  // e8m0 of 1: the instruction's own scales are not used
 
 __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
@@ -86,11 +86,9 @@ struct Rows {
 // Few rows: the work is reading b once.  A block computes 16 MS rows x 16 NS
 // columns, its KS waves taking every KS-th K block, so that together they read
 // KS * 128 consecutive bytes of each of b's rows; operands go straight from
-// memory to registers, kRing K blocks ahead, and the waves' sums are added in
+// memory to registers, RING K blocks ahead, and the waves' sums are added in
 // wave order through LDS.
-constexpr int kRing = 4;
-
-template <int KS, int MS, int NS, bool GROUPED, bool BBLOCK, bool F32>
+template <int KS, int MS, int NS, int RING, bool GROUPED, bool BBLOCK, bool F32>
 __global__ __launch_bounds__(64 * KS) void fp8_matmul_rows_kernel(Fp8MatmulArgs g) {
   __shared__ f32x4 part[KS][MS * NS][64];
   const int lane = threadIdx.x & 63;
@@ -123,7 +121,7 @@ __global__ __launch_bounds__(64 * KS) void fp8_matmul_rows_kernel(Fp8MatmulArgs 
     u32x4 a[MS][2], b[NS][2];
     float sa[MS], sb;
   };
-  Step ring[kRing];
+  Step ring[RING];
   auto load = [&](Step& st, int kb) {
     const size_t at = (size_t)kb * 128;
 #pragma unroll
@@ -164,12 +162,12 @@ __global__ __launch_bounds__(64 * KS) void fp8_matmul_rows_kernel(Fp8MatmulArgs 
     }
   };
 #pragma unroll
-  for (int u = 0; u < kRing; u++)
+  for (int u = 0; u < RING; u++)
     if (wave + u * KS < g.KB) load(ring[u], wave + u * KS);
-  for (int k0 = wave; k0 < g.KB; k0 += kRing * KS) {
+  for (int k0 = wave; k0 < g.KB; k0 += RING * KS) {
 #pragma unroll
-    for (int u = 0; u < kRing; u++) {
-      const int kb = k0 + u * KS, next = kb + kRing * KS;
+    for (int u = 0; u < RING; u++) {
+      const int kb = k0 + u * KS, next = kb + RING * KS;
       if (kb < g.KB) {
         compute(ring[u], kb);
         if (next < g.KB) load(ring[u], next);
@@ -209,21 +207,27 @@ template <int MS, bool GROUPED, bool BBLOCK, bool F32>
 hipError_t launch_rows(const Fp8MatmulArgs& g, hipStream_t s) {
   const int mt = (g.M + 16 * MS - 1) / (16 * MS);
   if (mt > 65535) return hipErrorInvalidValue;
-  // Two sub-tiles of columns per block where that still gives every CU two
-  // blocks; eight waves where each has a K block to itself.
-  const bool two = (long long)mt * ((g.N + 31) / 32) >= 2 * device_cu_count();
-  const bool eight = g.KB >= 8;
-#define QMOE_CALL(KS, NS)                                                                      \
-  hipLaunchKernelGGL((fp8_matmul_rows_kernel<KS, MS, NS, GROUPED, BBLOCK, F32>),               \
+  // Where 32-column blocks fill the chip twice, four waves of two sub-tiles
+  // hold the most bytes under way per CU (64 tokens x 128 experts x 8 picks of
+  // 1536 x 2048: 67 us against 94 us with eight waves); else the latency of one
+  // block counts and K is split further, one sub-tile per block (1 x 2048 x
+  // 2048: 3.7 against 4.9 us), two where many rows of a would be read again by
+  // every block (16 x 8192 x 4096: 8.9 against 10.2 us).
+  const long long blocks2 = (long long)mt * ((g.N + 31) / 32);
+  const int cus = device_cu_count();
+#define QMOE_CALL(KS, NS, RING)                                                                \
+  hipLaunchKernelGGL((fp8_matmul_rows_kernel<KS, MS, NS, RING, GROUPED, BBLOCK, F32>),         \
                      dim3((g.N + 16 * NS - 1) / (16 * NS), mt), dim3(64 * KS), 0, s, g)
-  if (two && eight)
-    QMOE_CALL(8, 2);
-  else if (two)
-    QMOE_CALL(4, 2);
-  else if (eight)
-    QMOE_CALL(8, 1);
+  if (blocks2 >= 2 * cus && (GROUPED || g.KB < 32))
+    QMOE_CALL(4, 2, 2);
+  else if (g.KB >= 32 && blocks2 >= cus && g.M > 8)
+    QMOE_CALL(16, 2, 1);
+  else if (g.KB >= 32)
+    QMOE_CALL(16, 1, 1);
+  else if (g.KB >= 8)
+    QMOE_CALL(8, 1, 2);
   else
-    QMOE_CALL(4, 1);
+    QMOE_CALL(4, 1, 2);
 #undef QMOE_CALL
   return hipGetLastError();
 }
@@ -273,9 +277,10 @@ __device__ inline void block_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int EU_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+  static constexpr int EU = EU_;  // waves per SIMD that the registers allow for
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int SM = BM / WM / 32, SN = BN / WN / 32;
   static constexpr int AC = BM / 8 / WAVES, BC = BN / 8 / WAVES;  // copies per wave and K block
@@ -285,21 +290,69 @@ struct Tile {
   static constexpr int B_AT = BM * 128, S_AT = B_AT + BN * 128, STAGE = S_AT + WAVES * 256;
   static_assert(SM * WM * 32 == BM && SN * WN * 32 == BN, "whole sub-tiles");
   static_assert(AC * WAVES * 8 == BM && BC * WAVES * 8 == BN, "whole copies");
-  static_assert(AS + (BN + 63) / 64 <= WAVES, "one scale copy per wave");
   static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
+};
+
+// The row tiles of the experts, found by every wave from expert_offsets: a
+// lane holds the tiles of E / 64 consecutive experts, a prefix sum over the
+// lanes places them.
+template <int BM>
+struct Spans {
+  int first, mine, per;  // tiles before this lane's experts, its own, experts per lane
+  __device__ inline int tiles(const Fp8MatmulArgs& g, int e) const {
+    return (g.expert_offsets[e + 1] - g.expert_offsets[e] + BM - 1) / BM;
+  }
+  __device__ inline int count(const Fp8MatmulArgs& g) {
+    const int lane = threadIdx.x & 63;
+    per = (g.E + 63) / 64;
+    mine = 0;
+    for (int i = 0; i < per; i++)
+      if (lane * per + i < g.E) mine += tiles(g, lane * per + i);
+    int sum = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int v = __shfl_up(sum, off, 64);
+      if (lane >= off) sum += v;
+    }
+    first = sum - mine;
+    return __builtin_amdgcn_readlane(sum, 63);
+  }
+  // Expert and rows [*m0, *mend) of row tile t (below count).
+  __device__ inline int find(const Fp8MatmulArgs& g, int t, int* m0, int* mend) const {
+    const unsigned long long at = __ballot(first <= t && t < first + mine);
+    const int lane = (int)__ffsll(at) - 1;
+    int left = t - __builtin_amdgcn_readlane(first, lane);
+    const int per_lane = __builtin_amdgcn_readfirstlane(per);
+    int e = lane * per_lane;
+    for (int i = 0; i + 1 < per_lane && left >= tiles(g, e); i++) left -= tiles(g, e++);
+    *m0 = g.expert_offsets[e] + left * BM;
+    *mend = min(*m0 + BM, g.expert_offsets[e + 1]);
+    return e;
+  }
+};
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
 };
 
 // OUT32: out is fp32 (the sums of a K split, and fp32 outputs); EXACT: the
 // codes are widened to bf16.  blockIdx.y is the part of a K split.
 template <class C, bool GROUPED, bool BBLOCK, bool EXACT, bool OUT32>
-__global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8MatmulArgs g) {
+__global__ __launch_bounds__(C::THREADS, C::EU) void fp8_matmul_tile_kernel(Fp8MatmulArgs g) {
   constexpr int SM = C::SM, SN = C::SN;
+  static_assert(C::AS + (BBLOCK ? 1 : (C::BN + 63) / 64) <= C::WAVES, "one scale copy per wave");
   __shared__ __align__(1024) uint8_t lds[C::STAGES * C::STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
   const int ntn = (g.N + C::BN - 1) / C::BN;
-  const int ntm = ((GROUPED ? *g.num_padded : g.M) + C::BM - 1) / C::BM;
+  // Grouped: a row tile is up to BM rows of one expert, however many of
+  // qmoe_align's tiles they are, so that the expert's matrix is read as seldom
+  // as BM allows.
+  Spans<C::BM> spans;
+  int ntm = (g.M + C::BM - 1) / C::BM;
+  if constexpr (GROUPED) ntm = spans.count(g);
   // The launch order deals blocks to the XCDs in turn: give each XCD a
   // contiguous run of tiles, column-tile by column-tile inside bands of
   // kBand row tiles, so that its L2 sees the same rows again.
@@ -309,16 +362,29 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   if (id >= total || (int)(blockIdx.x / 8) >= per) return;  // also past the tiles in use
   const int band = id / (kBand * ntn), in = id - band * kBand * ntn;
   const int rows = min(kBand, ntm - band * kBand);
-  const int m0 = (band * kBand + in % rows) * C::BM, n0 = in / rows * C::BN;
+  const int mt = band * kBand + in % rows, n0 = in / rows * C::BN;
+  int m0 = mt * C::BM, mend = g.M;
   const int kb0 = blockIdx.y * g.split_kb, kb1 = min(g.KB, kb0 + g.split_kb);
   const int NB = (g.N + 127) / 128;
   const uint8_t* b = g.b;
   const float* bs = g.b_scale;
   if constexpr (GROUPED) {
-    const int e = g.tile_expert[m0 / g.block_m];
-    if (e < 0) return;
+    const int e = spans.find(g, mt, &m0, &mend);
     b += (size_t)e * g.N * g.K;
     bs += (size_t)e * NB * g.KB;
+  }
+  auto out_row = [&](int slot) {
+    return GROUPED && slot >= mend ? -1 : Rows<GROUPED>::out_row(g, slot);
+  };
+  // The wave's sub-tiles of rows are wm, wm + WM, ...; those with rows come
+  // first (an expert's rows stand in front of its padding).
+  int live = SM;
+  if constexpr (GROUPED) {
+    live = 0;
+#pragma unroll
+    for (int s = 0; s < SM; s++)
+      live += out_row(m0 + (s * C::WM + wm) * 32) >= 0;
+    live = __builtin_amdgcn_readfirstlane(live);
   }
   // Copies: 8 lanes per row, the rows of a wave's copy t being 8 t .. 8 t + 7.
   // The chunk order alternates with t, hence two lane offsets where the rows
@@ -336,8 +402,9 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
 #pragma unroll
     for (int i = 0; i < C::AC; i++) {
       const int t = wave * C::AC + i;
-      const int row = Rows<true>::a_row(g, Rows<true>::out_row(g, m0 + t * 8 + (lane >> 3)));
-      av[i] = (unsigned)row * (unsigned)g.K + swz(t);
+      const int o = out_row(m0 + t * 8 + (lane >> 3));
+      // no row: behind every buffer, so nothing is read
+      av[i] = o < 0 ? kNowhere : (unsigned)Rows<true>::a_row(g, o) * (unsigned)g.K + swz(t);
     }
   } else {
     av[0] = bv[0];
@@ -352,9 +419,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   if (wave < C::AS) {
     sbase = reinterpret_cast<const uint8_t*>(g.a_scale);
     sstep = sbytes = (size_t)g.Ma * 4;
-    const int slot = m0 + wave * 64 + lane;
-    const bool in_tile = wave * 64 + lane < C::BM;
-    sv = in_tile ? 4u * (unsigned)Rows<GROUPED>::a_row(g, Rows<GROUPED>::out_row(g, slot)) : 0u;
+    const int o = wave * 64 + lane < C::BM ? out_row(m0 + wave * 64 + lane) : -1;
+    sv = 4u * (unsigned)Rows<GROUPED>::a_row(g, o);
   } else if constexpr (BBLOCK) {
     if (wave == C::AS) {
       sbytes = (size_t)NB * g.KB * 4;
@@ -411,7 +477,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   // One K block from stage st; the copies of K block kb + STAGES - 1 (to nx)
   // are issued between the matrix instructions, so that no wave waits in front
   // of them for the memory pipe to take its copies.
-  auto compute = [&](const uint8_t* st, uint8_t* nx, int kb) {
+  auto compute = [&](auto live_, const uint8_t* st, uint8_t* nx, int kb) {
+    constexpr int LIVE = decltype(live_)::value;  // sub-tile rows to compute
     const uint8_t* la = st;
     const uint8_t* lb = st + C::B_AT;
     const float* ls = reinterpret_cast<const float*>(st + C::S_AT);
@@ -419,7 +486,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
     float sa[SM];
     const float sb = BBLOCK ? ls[C::AS * 64 + nblk] : 1.0f;
 #pragma unroll
-    for (int s = 0; s < SM; s++) sa[s] = ls[(wm * SM + s) * 32 + r32] * sb;
+    for (int s = 0; s < SM; s++) sa[s] = ls[(s * C::WM + wm) * 32 + r32] * sb;
     f32x4 sbn[BBLOCK ? 1 : SN][4];  // b's scales of the lane's 16 columns per sub-tile
     if constexpr (!BBLOCK) {
 #pragma unroll
@@ -438,14 +505,17 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
           acc[i][s][r] = __builtin_fmaf(t[r] * sbn[i][r >> 2][r & 3], sa[s], acc[i][s][r]);
       }
     };
-    if constexpr (EXACT) {
+    if constexpr (LIVE == 0) {
+#pragma unroll
+      for (int u = 0; u < C::COPIES; u++) load(nx, next, u);
+    } else if constexpr (EXACT) {
       // The codes widened to bf16, 16 positions of K per instruction: a lane's
       // chunk of 16 codes feeds two.
       f32x16 t[SN][SM];
 #pragma unroll
       for (int i = 0; i < SN; i++)
 #pragma unroll
-        for (int s = 0; s < SM; s++)
+        for (int s = 0; s < LIVE; s++)
 #pragma unroll
           for (int r = 0; r < 16; r++) t[i][s][r] = 0.f;
 #pragma unroll
@@ -456,20 +526,20 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
         for (int i = 0; i < SN; i++)
           y[i] = *reinterpret_cast<const u32x4*>(lb + (wn * SN + i) * 4096 + o);
 #pragma unroll
-        for (int s = 0; s < SM; s++)
-          x[s] = *reinterpret_cast<const u32x4*>(la + (wm * SM + s) * 4096 + o);
+        for (int s = 0; s < LIVE; s++)
+          x[s] = *reinterpret_cast<const u32x4*>(la + (s * C::WM + wm) * 4096 + o);
 #pragma unroll
         for (int u = c * C::COPIES / 4; u < (c + 1) * C::COPIES / 4; u++) load(nx, next, u);
 #pragma unroll
         for (int j = 0; j < 2; j++) {
           bf16x8 xs[SM];
 #pragma unroll
-          for (int s = 0; s < SM; s++) xs[s] = widen8(x[s][2 * j], x[s][2 * j + 1]);
+          for (int s = 0; s < LIVE; s++) xs[s] = widen8(x[s][2 * j], x[s][2 * j + 1]);
 #pragma unroll
           for (int i = 0; i < SN; i++) {
             const bf16x8 ys = widen8(y[i][2 * j], y[i][2 * j + 1]);
 #pragma unroll
-            for (int s = 0; s < SM; s++)
+            for (int s = 0; s < LIVE; s++)
               t[i][s] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ys, xs[s], t[i][s], 0, 0, 0);
           }
         }
@@ -477,7 +547,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
 #pragma unroll
       for (int i = 0; i < SN; i++)
 #pragma unroll
-        for (int s = 0; s < SM; s++) scaled(t[i][s], i, s);
+        for (int s = 0; s < LIVE; s++) scaled(t[i][s], i, s);
     } else {
       i32x8 bf[SN][2];
 #pragma unroll
@@ -486,8 +556,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
         for (int j = 0; j < 2; j++) bf[i][j] = frag(lb, wn * SN + i, j);
       f32x16 t[2];
 #pragma unroll
-      for (int s = 0; s < SM; s++) {
-        const i32x8 x0 = frag(la, wm * SM + s, 0), x1 = frag(la, wm * SM + s, 1);
+      for (int s = 0; s < LIVE; s++) {
+        const i32x8 x0 = frag(la, s * C::WM + wm, 0), x1 = frag(la, s * C::WM + wm, 1);
 #pragma unroll
         for (int i = 0; i < SN; i++) {
           const int q = s * SN + i;
@@ -499,7 +569,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
           z = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(bf[i][1], x1, z, 0, 0, 0, kUnit, 0,
                                                               kUnit);
           t[q & 1] = z;
-          constexpr int kParts = (SM * SN + 1) / 2;  // all copies by the middle of the step
+          constexpr int kParts = (LIVE * SN + 1) / 2;  // all copies by the middle of the step
 #pragma unroll
           for (int u = 0; u < C::COPIES; u++)
             if (u * kParts / C::COPIES == q) load(nx, next, u);
@@ -507,26 +577,39 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
           if (q > 0) scaled(t[(q - 1) & 1], (q - 1) % SN, (q - 1) / SN);
         }
       }
-      scaled(t[(SM * SN - 1) & 1], SN - 1, SM - 1);
+      scaled(t[(LIVE * SN - 1) & 1], SN - 1, LIVE - 1);
     }
   };
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; s++)
 #pragma unroll
     for (int u = 0; u < C::COPIES; u++) load(lds + s * C::STAGE, kb0 + s, u);
-  for (int kb = kb0;;) {
-    bool done = false;
+  auto k_loop = [&](auto live_) {
+    for (int kb = kb0;;) {
+      bool done = false;
 #pragma unroll
-    for (int s = 0; s < C::STAGES; s++) {
-      if (done) continue;
-      // Stage s has landed (the stages behind it may be under way), in every
-      // wave; and every wave is done with the stage before, which is free now.
-      wait_memory<(C::STAGES - 2) * C::COPIES>();
-      block_barrier();
-      compute(lds + s * C::STAGE, lds + (s + C::STAGES - 1) % C::STAGES * C::STAGE, kb);
-      done = ++kb >= kb1;
+      for (int s = 0; s < C::STAGES; s++) {
+        if (done) continue;
+        // Stage s has landed (the stages behind it may be under way), in every
+        // wave; and every wave is done with the stage before, which is free now.
+        wait_memory<(C::STAGES - 2) * C::COPIES>();
+        block_barrier();
+        compute(live_, lds + s * C::STAGE, lds + (s + C::STAGES - 1) % C::STAGES * C::STAGE, kb);
+        done = ++kb >= kb1;
+      }
+      if (done) break;
     }
-    if (done) break;
+  };
+  if constexpr (GROUPED) {  // (the same number of barriers in every one)
+    switch (live) {
+      case 0: k_loop(Int<0>{}); break;
+      case 1: k_loop(Int<1>{}); break;
+      case 2: if constexpr (SM >= 2) k_loop(Int<2>{}); break;
+      case 3: if constexpr (SM >= 3) k_loop(Int<3>{}); break;
+      default: if constexpr (SM >= 4) k_loop(Int<4>{}); break;
+    }
+  } else {
+    k_loop(Int<SM>{});
   }
   wait_memory<0>();  // no copy is under way when LDS is used again, or ends
 
@@ -546,7 +629,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
     for (int s = 0; s < SM; s++)
 #pragma unroll
       for (int u = 0; u < 32 / RPI; u++)
-        orow[s][u] = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + u * RPI + lane / PIECES);
+        orow[s][u] = out_row(m0 + (s * C::WM + wm) * 32 + u * RPI + lane / PIECES);
     __syncthreads();  // the last K block has been read
     uint8_t* const mine = lds + wave * 32 * RB;
 #pragma unroll
@@ -577,7 +660,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void fp8_matmul_tile_kernel(Fp8Matmu
   }
 #pragma unroll
   for (int s = 0; s < SM; s++) {
-    const int orow = Rows<GROUPED>::out_row(g, m0 + (wm * SM + s) * 32 + r32);
+    const int orow = out_row(m0 + (s * C::WM + wm) * 32 + r32);
     if (orow < 0) continue;
     const size_t o = (size_t)orow * g.N;
 #pragma unroll
@@ -617,8 +700,9 @@ __global__ __launch_bounds__(256) void fp8_matmul_sum_kernel(const float* __rest
 
 template <class C, bool GROUPED, bool BBLOCK, bool EXACT>
 hipError_t launch_tile(Fp8MatmulArgs g, int splits, hipStream_t s) {
-  const long long total =
-      (long long)((g.N + C::BN - 1) / C::BN) * ((g.M + C::BM - 1) / C::BM);
+  // Grouped: at most one row tile per BM rows and one more per expert.
+  const long long ntm = GROUPED ? g.M / C::BM + (g.E < g.P ? g.E : g.P) : (g.M + C::BM - 1) / C::BM;
+  const long long total = (long long)((g.N + C::BN - 1) / C::BN) * ntm;
   if (total > (1ll << 30)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((total + 7) / 8 * 8), splits), block(C::THREADS);
   g.split_kb = (g.KB + splits - 1) / splits;
@@ -647,20 +731,47 @@ hipError_t launch_tile(Fp8MatmulArgs g, int splits, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The tiles, from the sharpest reuse of what a CU copies (64 KiB of operands
+// feed 32 x 2 matrix instructions per SIMD in Big, 16 KiB 2 in Small) to the
+// most blocks and the shortest latency.
 typedef Tile<256, 256, 2, 4, 2> Big;
+typedef Tile<128, 256, 2, 4, 3> Wide;
 typedef Tile<128, 128, 2, 2, 2> Mid;
+typedef Tile<64, 128, 2, 2, 3> Half;
 typedef Tile<64, 64, 2, 2, 4> Small;
+typedef Tile<32, 128, 1, 4, 2> Low;
+typedef Tile<32, 128, 1, 4, 3> LowFew;
+enum { kRows, kSmall, kHalf, kMid, kBig };
 
-// Tile (0 few rows, 1 small, 2 middle, 3 big) and parts of K of a dense product.
+// Kernel and parts of K of a dense product: the largest tile that still gives
+// every CU its blocks (two per CU, one of Big's), measured (us) as
+//   rows x columns x K      Small  Half   Mid    Big
+//   512 x 2048 x 2048         8.4   9.6   14.5
+//   2048 x 2048 x 2048       18.9  14.7   16.0   29.0
+//   2048 x 4096 x 4096       63.3  47.2   37.7   53.3
+//   4096 x 4096 x 1024       39.9  28.1   23.5   22.5
+// Mid's rounds over the chip cost 1 where Big's cost 1.9.  Where Small's tiles
+// leave CUs without work, K is split in up to 8 parts of 6 K blocks or more
+// (33 x 4096 x 4096: 9.3 us in four parts, 12 in one), which a second launch
+// adds.
 struct Plan {
-  int tile, splits;
+  int kernel, splits;
 };
 Plan plan(int M, int N, int K, bool big) {
-  const int force = getenv("QT") ? atoi(getenv("QT")) : -1, fs = getenv("QS") ? atoi(getenv("QS")) : 1;
-  if (force >= 0) return {force, fs};
-  if (M <= 32) return {0, 1};
-  if (big && (long long)((M + 255) / 256) * ((N + 255) / 256) >= 200) return {3, 1};
-  return {2, 1};
+  if (M <= 32) return {kRows, 1};
+  const int KB = K / 128, cus = device_cu_count();
+  auto tiles = [&](int bm, int bn) {
+    return (long long)((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+  };
+  if (tiles(64, 64) <= 2 * cus) {
+    int s = 8;
+    while (s > 1 && (tiles(64, 64) * s > cus || KB / s < 6)) s /= 2;
+    return {kSmall, s};
+  }
+  if (tiles(64, 128) <= 2 * cus) return {kHalf, 1};
+  const long long mid = (tiles(128, 128) + 2 * cus - 1) / (2 * cus);
+  const long long wide = (tiles(256, 256) + cus - 1) / cus;
+  return {big && 1.9 * wide <= mid ? kBig : kMid, 1};
 }
 
 }  // namespace
@@ -674,38 +785,47 @@ size_t fp8_matmul_parts_bytes(int M, int N, int K) {
 namespace {
 template <bool BBLOCK, bool EXACT>
 hipError_t dense(const Fp8MatmulArgs& g, hipStream_t s) {
+  // (Big is built for the products that reach its size: weights, bf16.)
   const Plan p = plan(g.M, g.N, g.K, BBLOCK && !EXACT);
-  if (p.tile == 0) {
-    return g.M <= 16 ? launch_rows<1, false, BBLOCK, EXACT>(g, s)
-                     : launch_rows<2, false, BBLOCK, EXACT>(g, s);
-  }
   if constexpr (BBLOCK && !EXACT) {
-    if (p.tile == 3) return launch_tile<Big, false, true, false>(g, p.splits, s);
+    if (p.kernel == kBig) return launch_tile<Big, false, true, false>(g, p.splits, s);
   }
-  if (p.tile == 1) return launch_tile<Small, false, BBLOCK, EXACT>(g, p.splits, s);
-  if constexpr (!EXACT) if (p.tile == 4) return launch_tile<Tile<128,256,2,4,3>, false, BBLOCK, EXACT>(g, p.splits, s);
-  if constexpr (!EXACT) if (p.tile == 5) return launch_tile<Tile<256,128,4,2,3>, false, BBLOCK, EXACT>(g, p.splits, s);
-  if (p.tile == 6) return launch_tile<Tile<64,128,2,2,3>, false, BBLOCK, EXACT>(g, p.splits, s);
-  if (getenv("QM")) return launch_tile<Tile<128,128,2,2,4>, false, BBLOCK, EXACT>(g, p.splits, s);
-  return launch_tile<Mid, false, BBLOCK, EXACT>(g, p.splits, s);
+  switch (p.kernel) {
+    case kRows:
+      return g.M <= 16 ? launch_rows<1, false, BBLOCK, EXACT>(g, s)
+                       : launch_rows<2, false, BBLOCK, EXACT>(g, s);
+    case kSmall: return launch_tile<Small, false, BBLOCK, EXACT>(g, p.splits, s);
+    case kHalf: return launch_tile<Half, false, BBLOCK, EXACT>(g, p.splits, s);
+    default: return launch_tile<Mid, false, BBLOCK, EXACT>(g, p.splits, s);
+  }
 }
 
+// By the mean rows per expert: the tile that holds most experts' rows at once,
+// so that a matrix is read once (128 experts of 1536 x 2048, top-8, us):
+//   tokens (mean)   rows16   Low   Half  Wide  Mid   Big
+//   64 (4)            68      74    77
+//   256 (16)         104      77    80          108
+//   512 (32)                  90    84    86     92   102
+//   1024 (64)                131   108    96    101   109
+//   2048 (128)                            130   142   124
+// and a smaller one where that leaves CUs without a block.
 template <bool EXACT>
 hipError_t grouped(const Fp8MatmulArgs& g, hipStream_t s) {
-  const char*q=getenv("QG");
-  if (g.block_m == 128) {
-  if(q&&q[0]=='1') return launch_tile<Tile<128,128,2,2,4>, true, true, EXACT>(g, 1, s);
-  if(q&&q[0]=='2') return launch_tile<Tile<128,128,2,2,3>, true, true, EXACT>(g, 1, s);
-  if constexpr(!EXACT) if(q&&q[0]=='3') return launch_tile<Tile<128,256,2,4,3>, true, true, EXACT>(g, 1, s);
-  return launch_tile<Mid, true, true, EXACT>(g, 1, s);
+  const double mean = (double)g.P / g.E;
+  const int cus = device_cu_count();
+  if (g.block_m == 16 && mean <= 6) return launch_rows<1, true, true, EXACT>(g, s);
+  auto blocks = [&](int bm, int bn) {  // experts that have rows, and full tiles
+    return ((double)g.P / bm + (g.E < g.P ? g.E : g.P) * 0.5) * ((g.N + bn - 1) / bn);
+  };
+  if constexpr (EXACT) {  // (its sums of a K block need the registers of a smaller tile)
+    if (mean > 48 && blocks(128, 128) >= 2 * cus) return launch_tile<Mid, true, true, true>(g, 1, s);
+  } else {
+    if (mean > 96 && blocks(256, 256) >= 2 * cus) return launch_tile<Big, true, true, false>(g, 1, s);
+    if (mean > 48 && blocks(128, 256) >= 2 * cus) return launch_tile<Wide, true, true, false>(g, 1, s);
   }
-  if (g.block_m == 64) return launch_tile<Tile<64, 128, 1, 4, 3>, true, true, EXACT>(g, 1, s);
-  if (g.block_m == 32) {
-  if(q&&q[0]=='1') return launch_tile<Tile<32, 128, 1, 4, 2>, true, true, EXACT>(g, 1, s);
-  if(q&&q[0]=='2') return launch_tile<Tile<32, 128, 1, 4, 4>, true, true, EXACT>(g, 1, s);
-  return launch_tile<Tile<32, 128, 1, 4, 3>, true, true, EXACT>(g, 1, s);
-  }
-  return launch_rows<1, true, true, EXACT>(g, s);
+  if (mean > 20 && blocks(64, 128) >= cus) return launch_tile<Half, true, true, EXACT>(g, 1, s);
+  return blocks(32, 128) >= 2 * cus ? launch_tile<Low, true, true, EXACT>(g, 1, s)
+                                    : launch_tile<LowFew, true, true, EXACT>(g, 1, s);
 }
 }  // namespace
 

@@ -129,7 +129,7 @@ def _lib() -> ctypes.CDLL:
             ("qmoe_fp8_matmul_workspace", sz, [i32] * 3),
             ("qmoe_fp8_matmul", ctypes.c_int, [vp] * 4 + [i32] * 4 + [vp, i32, vp, sz, vp]),
             ("qmoe_fp8_grouped_matmul", ctypes.c_int,
-             [vp, vp, i32] + [vp] * 5 + [i32] * 6 + [vp, i32, vp]),
+             [vp, vp, i32] + [vp] * 6 + [i32] * 6 + [vp, i32, vp]),
             ("qmoe_balance_workspace", sz, [i32] * 2),
             ("qmoe_balance", ctypes.c_int, [vp] * 3 + [i32] * 3 + [f32] + [vp] * 5 + [sz, vp]),
             ("qmoe_balance_backward", ctypes.c_int, [vp] * 5 + [i32] * 3 + [f32, vp, vp]),
@@ -640,13 +640,14 @@ def fp8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
     _need(cap > 0, "bad sizes: T %d, k %d, E %d, block_m %d", T, k, E, bm)
     _tensor(al["sorted_pair_ids"], "sorted_pair_ids", (cap,), torch.int32)
     _tensor(al["tile_expert"], "tile_expert", (cap // bm,), torch.int32)
+    _tensor(al["expert_offsets"], "expert_offsets", (E + 1,), torch.int32)
     _tensor(al["num_padded"], "num_padded", (1,), torch.int32)
     dev = _one_device(a, a_scale, b, b_scale, al["sorted_pair_ids"], al["tile_expert"],
-                      al["num_padded"], out)
+                      al["expert_offsets"], al["num_padded"], out)
     out = _out(out, (T * k, N), out_dtype, dev)
     _call(dev, "qmoe_fp8_grouped_matmul", _addr(a), _addr(a_scale), int(pair_rows), _addr(b),
           _addr(b_scale), _addr(al["sorted_pair_ids"]), _addr(al["tile_expert"]),
-          _addr(al["num_padded"]), T, k, E, bm, N, K, _addr(out), _float_kind(out, "out"))
+          _addr(al["expert_offsets"]), _addr(al["num_padded"]), T, k, E, bm, N, K, _addr(out), _float_kind(out, "out"))
     return out
 
 

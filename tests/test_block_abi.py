@@ -66,12 +66,12 @@ def test_fp8_matmul_refusals():
 
 def test_fp8_grouped_matmul_refusals():
     c = _caller("qmoe_fp8_grouped_matmul", a=P, a_scale=P, pair_rows=0, b=P, b_scale=P, srt=P,
-                te=P, npad=P, T=4, k=2, E=8, block_m=16, N=64, K=256, out=P, out_dtype=0,
+                te=P, off=P, npad=P, T=4, k=2, E=8, block_m=16, N=64, K=256, out=P, out_dtype=0,
                 stream=None)
     for bad in (dict(pair_rows=2), dict(T=-1), dict(k=0), dict(k=9), dict(E=0), dict(block_m=48),
                 dict(N=0), dict(K=64), dict(K=0), dict(out_dtype=5), dict(T=1 << 30), dict(a=None),
                 dict(a_scale=None), dict(b=None), dict(b_scale=None), dict(srt=None),
-                dict(te=None), dict(npad=None), dict(out=None), dict(a=ODD), dict(b=ODD)):
+                dict(te=None), dict(off=None), dict(npad=None), dict(out=None), dict(a=ODD), dict(b=ODD)):
         assert c(**bad) == INV, bad
     assert c(E=2000) == UNS
     assert c(T=0, a=None) == OK
