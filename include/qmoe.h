@@ -431,8 +431,9 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
  *   is still a kept token); NaN or +inf in a kept row makes the loss NaN.
  * logits fp32 [T,E]; topk_ids int32 [T,k]; loss fp32 [1], counts int32 [E],
  *   probs fp32 [E], tokens int32 [1].  k <= 16, E <= 1024.
- * ws: qmoe_balance_workspace(T, E) bytes, 256-byte aligned, contents need no
- *   initialisation; calls that share it must be ordered on one stream.
+ * ws: qmoe_balance_workspace(T, E) bytes (0 for a small batch: ws may be
+ *   NULL), 256-byte aligned, contents need no initialisation; calls that
+ *   share it must be ordered on one stream.
  * qmoe_balance_backward -- the gradient of the loss to the logits, for the
  * counts and tokens of the forward call (the counts carry none):
  *   dlogits[t,e] = dloss * coef * E / n * p[t,e] * (f_e - sum_j f_j p[t,j]),

@@ -17,17 +17,19 @@ bool valid_dtype(int32_t d) { return d == QMOE_DT_BF16 || d == QMOE_DT_F32; }
 size_t elem(int32_t dtype) { return dtype == QMOE_DT_F32 ? 4 : 2; }
 bool valid_eps(float eps) { return eps > 0.0f && std::isfinite(eps); }
 
-// Workspace of qmoe_balance: partial sums, counts and kept tokens per block.
+// Workspace of qmoe_balance (none for a small batch).
 struct BalanceWs {
-  size_t psum, csum, nsum, total;
+  size_t psum, csum, nsum, terms, arrived, total;
 };
 BalanceWs balance_ws_layout(int T, int E) {
-  BalanceWs w;
+  BalanceWs w{};
+  if (balance_small(T, E)) return w;
   const size_t nb = balance_blocks(T);
-  w.psum = 0;
   w.csum = align_up(nb * E * 4, 256);
   w.nsum = align_up(w.csum + nb * E * 4, 256);
-  w.total = align_up(w.nsum + nb * 4, 256);
+  w.terms = align_up(w.nsum + nb * 4, 256);
+  w.arrived = align_up(w.terms + (size_t)((E + 63) / 64) * 8, 256);
+  w.total = w.arrived + 256;
   return w;
 }
 
@@ -171,16 +173,19 @@ qmoe_status qmoe_balance(const float* logits, const int32_t* topk_ids, const uin
   if (T < 0 || E < 1 || k < 1 || k > E || k > 16 || !std::isfinite(coef))
     return QMOE_ERR_INVALID_ARG;
   if (E > 1024) return QMOE_ERR_UNSUPPORTED;
-  if ((T > 0 && (!logits || !topk_ids)) || !loss || !counts || !probs || !tokens || !ws)
+  if ((T > 0 && (!logits || !topk_ids)) || !loss || !counts || !probs || !tokens)
     return QMOE_ERR_INVALID_ARG;
   const BalanceWs lay = balance_ws_layout(T, E);
-  if (ws_bytes < lay.total || !aligned(ws, 256)) return QMOE_ERR_INVALID_ARG;
+  if (lay.total > 0 && (!ws || ws_bytes < lay.total || !aligned(ws, 256)))
+    return QMOE_ERR_INVALID_ARG;
   uint8_t* w = reinterpret_cast<uint8_t*>(ws);
+  const BalanceParts parts{reinterpret_cast<float*>(w + lay.psum),
+                           reinterpret_cast<int32_t*>(w + lay.csum),
+                           reinterpret_cast<int32_t*>(w + lay.nsum),
+                           reinterpret_cast<double*>(w + lay.terms),
+                           reinterpret_cast<int32_t*>(w + lay.arrived)};
   return hip_status(launch_balance(logits, topk_ids, mask, T, E, k, coef, loss, counts, probs,
-                                   tokens, reinterpret_cast<float*>(w + lay.psum),
-                                   reinterpret_cast<int32_t*>(w + lay.csum),
-                                   reinterpret_cast<int32_t*>(w + lay.nsum),
-                                   (hipStream_t)stream));
+                                   tokens, parts, (hipStream_t)stream));
 }
 
 qmoe_status qmoe_balance_backward(const float* logits, const uint8_t* mask, const int32_t* counts,

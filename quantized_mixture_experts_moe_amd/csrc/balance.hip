@@ -24,8 +24,7 @@ __device__ inline void softmax_row(float z[EPL]) {
   float mx = z[0];
 #pragma unroll
   for (int i = 1; i < EPL; i++) mx = fmaxf(mx, z[i]);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor(mx, off, 64));
+  mx = wave_fmax(mx);
   const float m0 = mx == -INFINITY ? 0.f : mx;
   float sum = 0.f;
 #pragma unroll
@@ -46,77 +45,167 @@ __device__ inline void load_row(const float* row, int E, float z[EPL]) {
   for (int i = 0; i < EPL; i++) z[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
 }
 
-// One block's share of the tokens: partial probability sums psum[block][E],
-// counts csum[block][E] and kept tokens nsum[block].
-template <int EPL>
-__global__ __launch_bounds__(256) void balance_partial_kernel(
-    const float* __restrict__ logits, const int32_t* __restrict__ ids,
-    const uint8_t* __restrict__ mask, int T, int E, int k, float* __restrict__ psum,
-    int32_t* __restrict__ csum, int32_t* __restrict__ nsum) {
-  __shared__ float ps[4][64 * EPL];
-  __shared__ int hist[64 * EPL];
-  __shared__ int kept[4];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < 64 * EPL; e += 256) hist[e] = 0;
-  __syncthreads();
-  float acc[EPL];
+// A block's share of the tokens (WAVES waves, one token each at a time): the
+// probability sums in sum[e], e = threadIdx.x + WAVES * 64 * i, the counts in
+// hist, the kept tokens returned.  The next token's logits are loaded before
+// this one's are used.
+template <int EPL, int WAVES>
+struct Share {
+  float ps[WAVES][64 * EPL];
+  int hist[64 * EPL];
+  int kept[WAVES];
+
+  __device__ inline int run(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                            const uint8_t* __restrict__ mask, int T, int E, int k) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    for (int e = threadIdx.x; e < 64 * EPL; e += 64 * WAVES) hist[e] = 0;
+    __syncthreads();
+    float acc[EPL], z[EPL], nz[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; i++) acc[i] = 0.f;
-  int n = 0;
-  for (int t = blockIdx.x * 4 + wave; t < T; t += gridDim.x * 4) {
-    if (mask && mask[t] == 0) continue;  // the same for the whole wave
-    n++;
-    float z[EPL];
-    load_row<EPL>(logits + (size_t)t * E, E, z);
-    if (lane < k) {
-      const int e = ids[(size_t)t * k + lane];
-      if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+    for (int i = 0; i < EPL; i++) acc[i] = 0.f;
+    int n = 0;
+    const int step = gridDim.x * WAVES;
+    int t = blockIdx.x * WAVES + wave;
+    if (t < T) load_row<EPL>(logits + (size_t)t * E, E, nz);
+    for (; t < T; t += step) {
+#pragma unroll
+      for (int i = 0; i < EPL; i++) z[i] = nz[i];
+      if (t + step < T) load_row<EPL>(logits + (size_t)(t + step) * E, E, nz);
+      if (mask && mask[t] == 0) continue;  // the same for the whole wave
+      n++;
+      if (lane < k) {
+        const int e = ids[(size_t)t * k + lane];
+        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+      }
+      softmax_row<EPL>(z);
+#pragma unroll
+      for (int i = 0; i < EPL; i++) acc[i] += z[i];
     }
-    softmax_row<EPL>(z);
 #pragma unroll
-    for (int i = 0; i < EPL; i++) acc[i] += z[i];
+    for (int i = 0; i < EPL; i++) ps[wave][lane + 64 * i] = acc[i];
+    if (lane == 0) kept[wave] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; w++) n += kept[w];
+    return n;
   }
-#pragma unroll
-  for (int i = 0; i < EPL; i++) ps[wave][lane + 64 * i] = acc[i];
-  if (lane == 0) kept[wave] = n;
+};
+
+// Sum over the waves of a block, in every thread; `s` holds WAVES doubles.
+template <int WAVES>
+__device__ inline double block_sum64(double x, double* s) {
+  x = wave_sum64(x);
   __syncthreads();
-  for (int e = threadIdx.x; e < E; e += 256) {
-    psum[(size_t)blockIdx.x * E + e] = (ps[0][e] + ps[1][e]) + (ps[2][e] + ps[3][e]);
-    csum[(size_t)blockIdx.x * E + e] = hist[e];
-  }
-  if (threadIdx.x == 0) nsum[blockIdx.x] = kept[0] + kept[1] + kept[2] + kept[3];
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0.0;
+#pragma unroll
+  for (int w = 0; w < WAVES; w++) x += s[w];
+  return x;
 }
 
-// Sums the partials of nb blocks (one block of 1024 threads, one expert per
-// thread) and forms the loss.
-__global__ __launch_bounds__(1024) void balance_finish_kernel(
-    const float* __restrict__ psum, const int32_t* __restrict__ csum,
-    const int32_t* __restrict__ nsum, int nb, int E, int k, float coef, float* __restrict__ loss,
-    int32_t* __restrict__ counts, float* __restrict__ probs, int32_t* __restrict__ tokens) {
-  __shared__ double terms[16];
-  int n = 0;
-  for (int b = 0; b < nb; b++) n += nsum[b];
-  double term = 0.0;
-  for (int e = threadIdx.x; e < E; e += 1024) {
-    double p = 0.0;
-    int c = 0;
-    for (int b = 0; b < nb; b++) {
-      p += (double)psum[(size_t)b * E + e];
-      c += csum[(size_t)b * E + e];
+constexpr int kWaves = 8;  // of a partial block
+
+template <int EPL>
+__global__ __launch_bounds__(64 * kWaves) void balance_partial_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids,
+    const uint8_t* __restrict__ mask, int T, int E, int k, BalanceParts w) {
+  __shared__ Share<EPL, kWaves> share;
+  const int n = share.run(logits, ids, mask, T, E, k);
+  for (int e = threadIdx.x; e < E; e += 64 * kWaves) {
+    float s = share.ps[0][e];
+#pragma unroll
+    for (int v = 1; v < kWaves; v++) s += share.ps[v][e];
+    w.psum[(size_t)blockIdx.x * E + e] = s;
+    w.csum[(size_t)blockIdx.x * E + e] = share.hist[e];
+  }
+  if (threadIdx.x == 0) {
+    w.nsum[blockIdx.x] = n;
+    if (blockIdx.x == 0) *w.arrived = 0;
+  }
+}
+
+// Adds the partials of nb blocks: a block sums 64 experts, each of its 16
+// waves every 16th partial; the last block to arrive forms the loss from the
+// blocks' terms, in order.
+__global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceParts w, int nb, int E, int k,
+                                                              float coef, float* __restrict__ loss,
+                                                              int32_t* __restrict__ counts,
+                                                              float* __restrict__ probs,
+                                                              int32_t* __restrict__ tokens) {
+  __shared__ double ps[16][64], sums[16];
+  __shared__ int cs[16][64], last;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = blockIdx.x * 64 + lane;
+  const int n = (int)block_sum64<16>((int)threadIdx.x < nb ? (double)w.nsum[threadIdx.x] : 0.0, sums);
+  double p = 0.0;
+  int c = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int b = wave; b < nb; b += 16) {
+      p += (double)w.psum[(size_t)b * E + e];
+      c += w.csum[(size_t)b * E + e];
+    }
+  }
+  ps[wave][lane] = p;
+  cs[wave][lane] = c;
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int v = 1; v < 16; v++) {
+      p += ps[v][lane];
+      c += cs[v][lane];
     }
     p = n > 0 ? p / n : 0.0;
-    counts[e] = c;
-    probs[e] = (float)p;
-    if (n > 0) term += (double)c / ((double)k * n) * p;
+    double term = 0.0;
+    if (e < E) {
+      counts[e] = c;
+      probs[e] = (float)p;
+      if (n > 0) term = (double)c / ((double)k * n) * p;
+    }
+    term = wave_sum64(term);
+    if (lane == 0) {
+      w.terms[blockIdx.x] = term;
+      __threadfence();
+      last = atomicAdd(w.arrived, 1) == (int)gridDim.x - 1;
+      if (last) {
+        __threadfence();
+        double s = 0.0;
+        for (int b = 0; b < (int)gridDim.x; b++)
+          s += __hip_atomic_load(&w.terms[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        *loss = (float)((double)coef * E * s);
+        *tokens = n;
+      }
+    }
   }
+}
+
+// Small batches in one launch of one block.
+constexpr int kSmallWaves = 16;
+template <int EPL>
+__global__ __launch_bounds__(64 * kSmallWaves) void balance_small_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids,
+    const uint8_t* __restrict__ mask, int T, int E, int k, float coef, float* __restrict__ loss,
+    int32_t* __restrict__ counts, float* __restrict__ probs, int32_t* __restrict__ tokens) {
+  __shared__ Share<EPL, kSmallWaves> share;
+  __shared__ double sums[kSmallWaves];
+  const int n = share.run(logits, ids, mask, T, E, k);
+  double term = 0.0;
+  const int e = threadIdx.x;  // E <= 1024
+  if (e < E) {
+    double p = 0.0;
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) term += __shfl_xor(term, off, 64);
-  if ((threadIdx.x & 63) == 0) terms[threadIdx.x >> 6] = term;
-  __syncthreads();
+    for (int v = 0; v < kSmallWaves; v++) p += (double)share.ps[v][e];
+    p = n > 0 ? p / n : 0.0;
+    counts[e] = share.hist[e];
+    probs[e] = (float)p;
+    if (n > 0) term = (double)share.hist[e] / ((double)k * n) * p;
+  }
+  term = block_sum64<kSmallWaves>(term, sums);
   if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < 16; w++) s += terms[w];
-    *loss = (float)((double)coef * E * s);
+    *loss = (float)((double)coef * E * term);
     *tokens = n;
   }
 }
@@ -160,8 +249,11 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(
 
 }  // namespace
 
+// One block reads about 50 GB/s: up to 128 KiB of logits it is done before a
+// second launch could start.
+bool balance_small(int T, int E) { return (long long)T * E <= 32768; }
 int balance_blocks(int T) {
-  const int need = (T + 3) / 4;
+  const int need = (T + kWaves - 1) / kWaves;
   return need < 1 ? 1 : need > 256 ? 256 : need;
 }
 
@@ -174,17 +266,24 @@ int balance_blocks(int T) {
 
 hipError_t launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                           int E, int k, float coef, float* loss, int32_t* counts, float* probs,
-                          int32_t* tokens, float* psum, int32_t* csum, int32_t* nsum,
-                          hipStream_t s) {
+                          int32_t* tokens, const BalanceParts& w, hipStream_t s) {
+  if (balance_small(T, E)) {
+#define QMOE_CALL(EPL)                                                                           \
+  hipLaunchKernelGGL(balance_small_kernel<EPL>, dim3(1), dim3(64 * kSmallWaves), 0, s, logits,    \
+                     ids, mask, T, E, k, coef, loss, counts, probs, tokens);
+    QMOE_BALANCE_EPL(QMOE_CALL)
+#undef QMOE_CALL
+    return hipGetLastError();
+  }
   const int nb = balance_blocks(T);
-#define QMOE_CALL(EPL)                                                                         \
-  hipLaunchKernelGGL(balance_partial_kernel<EPL>, dim3(nb), dim3(256), 0, s, logits, ids, mask, \
-                     T, E, k, psum, csum, nsum);
+#define QMOE_CALL(EPL)                                                                          \
+  hipLaunchKernelGGL(balance_partial_kernel<EPL>, dim3(nb), dim3(64 * kWaves), 0, s, logits, ids, \
+                     mask, T, E, k, w);
   QMOE_BALANCE_EPL(QMOE_CALL)
 #undef QMOE_CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3(1), dim3(1024), 0, s, psum, csum, nsum, nb, E, k,
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((E + 63) / 64), dim3(1024), 0, s, w, nb, E, k,
                      coef, loss, counts, probs, tokens);
   return hipGetLastError();
 }

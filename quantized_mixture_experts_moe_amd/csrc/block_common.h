@@ -127,6 +127,26 @@ __device__ inline float wave_sum(float x) {
   return r;
 }
 
+// Maximum over the 64 lanes (NaN lanes are passed over), in every lane.
+__device__ inline float wave_fmax(float x) {
+  x = fmaxf(x, __uint_as_float(dpp<0xB1>(__float_as_uint(x))));
+  x = fmaxf(x, __uint_as_float(dpp<0x4E>(__float_as_uint(x))));
+  x = fmaxf(x, __uint_as_float(dpp<0x141>(__float_as_uint(x))));
+  x = fmaxf(x, __uint_as_float(dpp<0x140>(__float_as_uint(x))));
+  float r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 0));
+#pragma unroll
+  for (int row = 1; row < 4; row++)
+    r = fmaxf(r,
+              __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 16 * row)));
+  return r;
+}
+// Sum of doubles over the 64 lanes, the same in every lane.
+__device__ inline double wave_sum64(double x) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) x += __shfl_xor(x, off, 64);
+  return x;
+}
+
 __device__ inline uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // Scale of a group from its largest magnitude pattern: absmax / qmax, at

@@ -49,11 +49,21 @@ size_t fp8_matmul_parts_bytes(int M, int N, int K);
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s);
 hipError_t launch_fp8_grouped_matmul(const Fp8MatmulArgs& g, hipStream_t s);
 
-int balance_blocks(int T);  // blocks (partial sums) of the forward pass
+// Workspace of the balance loss: per block (balance_blocks) the probability
+// sums and counts [E] and kept tokens; per 64 experts a term of the loss; the
+// blocks that have arrived.  A small batch needs none.
+struct BalanceParts {
+  float* psum;
+  int32_t* csum;
+  int32_t* nsum;
+  double* terms;
+  int32_t* arrived;
+};
+bool balance_small(int T, int E);
+int balance_blocks(int T);
 hipError_t launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                           int E, int k, float coef, float* loss, int32_t* counts, float* probs,
-                          int32_t* tokens, float* psum, int32_t* csum, int32_t* nsum,
-                          hipStream_t s);
+                          int32_t* tokens, const BalanceParts& w, hipStream_t s);
 hipError_t launch_balance_backward(const float* logits, const uint8_t* mask,
                                    const int32_t* counts, const int32_t* tokens,
                                    const float* dloss, int T, int E, int k, float coef,

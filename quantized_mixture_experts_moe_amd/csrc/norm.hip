@@ -145,6 +145,29 @@ __device__ inline float rms_inv(float sumsq, int H, float eps) {
   return 1.0f / sqrtf(sumsq / (float)H + eps);
 }
 
+// The forward norms' r: the sum of squares in fp64 and the mean rounded once,
+// so that r, and with it every rounding decision behind it (the stored out,
+// the codes), does not depend on how a row is spread over threads.
+template <class S>
+__device__ inline float row_rms_inv(const float x[S::NV][8], int H, float eps, double* red) {
+  double s = 0.0;
+#pragma unroll
+  for (int v = 0; v < S::NV; v++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) s += (double)x[v][j] * (double)x[v][j];
+  s = wave_sum64(s);
+  if constexpr (S::WAVES > 1) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();  // the last use of `red`
+    if ((threadIdx.x & 63) == 0) red[w] = s;
+    __syncthreads();
+    s = red[0];
+#pragma unroll
+    for (int i = 1; i < S::WAVES; i++) s += red[i];
+  }
+  return rsqrtf((float)(s / H) + eps);
+}
+
 // Writes a row of normed values in the form asked for.  `grp` (LDS, 128
 // words) serves the column groups of rows that are not taken by vectors.
 template <class S>
@@ -235,7 +258,10 @@ __device__ inline void write_form(const NormForm& f, size_t row, bool live, int 
 
 template <class S>
 struct Lds {
-  float red[2 * (S::BLOCK / 64)];
+  union {
+    float red[2 * (S::BLOCK / 64)];
+    double red64[S::BLOCK / 64];
+  };
   uint32_t grp[128];
 };
 
@@ -250,7 +276,7 @@ __global__ __launch_bounds__(S::BLOCK) void pre_norm_kernel(const void* __restri
   float v[S::NV][8], wt[S::NV][8];
   load_row<S, F32>(x, live ? row : (size_t)T - 1, H, tr, v);
   load_row<S, true>(w, 0, H, tr, wt);
-  const float r = rms_inv(row_sum<S>(sum_sq<S>(v), lds.red), H, eps);
+  const float r = row_rms_inv<S>(v, H, eps, lds.red64);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
@@ -287,27 +313,27 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_kernel(
   const size_t row = (size_t)blockIdx.x * S::RPB + threadIdx.x / S::TPR;
   const bool live = row < (size_t)T;
   const size_t rd = live ? row : (size_t)T - 1;
-  float v[S::NV][8], g[S::NV][8], t[S::NV][8];
+  float v[S::NV][8], g[S::NV][8], t[S::NV][8], res[S::NV][8];
   load_row<S, F32>(y, rd, H, tr, v);
+  load_row<S, F32>(x, rd, H, tr, res);
   load_gate<S, F32, G>(gate, rd, H, tr, g);
   load_row<S, true>(w, 0, H, tr, t);
-  const float r = rms_inv(row_sum<S>(sum_sq<S>(v), lds.red), H, eps);
+  const float r = row_rms_inv<S>(v, H, eps, lds.red64);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
     for (int j = 0; j < 8; j++) g[i][j] *= v[i][j] * r * t[i][j];
-  load_row<S, F32>(x, rd, H, tr, v);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
     for (int j = 0; j < 8; j++) {
-      v[i][j] = alpha * v[i][j] + g[i][j];
+      v[i][j] = alpha * res[i][j] + g[i][j];
       if constexpr (!F32) v[i][j] = bf16_f32(f32_bf16(v[i][j]));  // as stored
     }
   if (live) store_row<S, F32>(out, row, H, tr, v);
   if (w2 == nullptr) return;
   load_row<S, true>(w2, 0, H, tr, t);
-  const float r2 = rms_inv(row_sum<S>(sum_sq<S>(v), lds.red), H, eps);
+  const float r2 = row_rms_inv<S>(v, H, eps, lds.red64);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
@@ -462,22 +488,28 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_backward_kernel(
 }
 
 // out[c] = sum over the nb rows of part[nb][H], in fp64: a block sums 64
-// columns, each of its four waves every fourth row.
-__global__ __launch_bounds__(256) void norm_colsum_kernel(const float* __restrict__ part0,
-                                                          float* __restrict__ out0,
-                                                          const float* __restrict__ part1,
-                                                          float* __restrict__ out1, int nb, int H) {
-  __shared__ double s[4][64];
+// columns, each of its 16 waves every 16th row.
+__global__ __launch_bounds__(1024) void norm_colsum_kernel(const float* __restrict__ part0,
+                                                           float* __restrict__ out0,
+                                                           const float* __restrict__ part1,
+                                                           float* __restrict__ out1, int nb,
+                                                           int H) {
+  __shared__ double s[16][64];
   const float* part = blockIdx.y == 0 ? part0 : part1;
   float* out = blockIdx.y == 0 ? out0 : out1;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = blockIdx.x * 64 + lane;
   double a = 0.0;
-  if (c < H)
-    for (int b = wave; b < nb; b += 4) a += (double)part[(size_t)b * H + c];
+  if (c < H) {
+#pragma unroll 8
+    for (int b = wave; b < nb; b += 16) a += (double)part[(size_t)b * H + c];
+  }
   s[wave][lane] = a;
   __syncthreads();
-  if (wave == 0 && c < H) out[c] = (float)((s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]));
+  if (wave != 0 || c >= H) return;
+#pragma unroll
+  for (int w = 1; w < 16; w++) a += s[w][lane];
+  out[c] = (float)a;
 }
 
 // Picks the shape for H: 64 threads per row up to 2048 columns, then 256 and
@@ -544,7 +576,7 @@ hipError_t post(const PostNormArgs& a, hipStream_t s) {
 
 hipError_t colsum(const float* p0, float* o0, const float* p1, float* o1, int nb, int H,
                   hipStream_t s) {
-  hipLaunchKernelGGL(norm_colsum_kernel, dim3((H + 63) / 64, p1 ? 2 : 1), dim3(256), 0, s, p0, o0,
+  hipLaunchKernelGGL(norm_colsum_kernel, dim3((H + 63) / 64, p1 ? 2 : 1), dim3(1024), 0, s, p0, o0,
                      p1, o1, nb, H);
   return hipGetLastError();
 }

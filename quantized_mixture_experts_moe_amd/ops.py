@@ -697,8 +697,8 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
     _tensor(logits, "logits", (T, E), torch.float32)
     _tensor(topk_ids, "topk_ids", (T, k), torch.int32)
     dev = _one_device(logits, topk_ids, mask, ws)
-    need = int(_lib().qmoe_balance_workspace(T, E))
-    if ws is None or ws.numel() * ws.element_size() < need:
+    need = _lib().qmoe_balance_workspace(T, E)
+    if need and (ws is None or ws.numel() * ws.element_size() < need):
         ws = _ws(need, dev)
     r = {"loss": torch.empty(1, dtype=torch.float32, device=dev),
          "counts": torch.empty(E, dtype=torch.int32, device=dev),
@@ -706,7 +706,7 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
          "tokens": torch.empty(1, dtype=torch.int32, device=dev)}
     _call(dev, "qmoe_balance", _addr(logits), _addr(topk_ids), _mask_ptr(mask, T), T, E, k, coef,
           _addr(r["loss"]), _addr(r["counts"]), _addr(r["probs"]), _addr(r["tokens"]), _addr(ws),
-          ws.numel() * ws.element_size())
+          0 if ws is None else ws.numel() * ws.element_size())
     return r
 
 

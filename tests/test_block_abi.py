@@ -79,9 +79,9 @@ def test_fp8_grouped_matmul_refusals():
 
 def test_balance_refusals():
     ws = ops.lib().qmoe_balance_workspace
-    n = ws(64, 8)
+    n = ws(6400, 8)
     assert n >= 256 and n % 256 == 0 and ws(-1, 8) == 0 and ws(4, 0) == 0
-    c = _caller("qmoe_balance", logits=P, ids=P, mask=None, T=64, E=8, k=2, coef=0.1, loss=P,
+    c = _caller("qmoe_balance", logits=P, ids=P, mask=None, T=6400, E=8, k=2, coef=0.1, loss=P,
                 counts=P, probs=P, tokens=P, ws=P, ws_bytes=n, stream=None)
     for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(E=64, k=17), dict(coef=NAN),
                 dict(coef=INF), dict(logits=None), dict(ids=None), dict(loss=None),
