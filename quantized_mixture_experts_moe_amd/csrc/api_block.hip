@@ -28,7 +28,7 @@ BalanceWs balance_ws_layout(int T, int E) {
   w.csum = align_up(nb * E * 4, 256);
   w.nsum = align_up(w.csum + nb * E * 4, 256);
   w.terms = align_up(w.nsum + nb * 4, 256);
-  w.arrived = align_up(w.terms + (size_t)((E + 63) / 64) * 8, 256);
+  w.arrived = align_up(w.terms + (size_t)((E + 31) / 32) * 8, 256);
   w.total = w.arrived + 256;
   return w;
 }

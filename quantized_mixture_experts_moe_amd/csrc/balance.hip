@@ -29,7 +29,7 @@ __device__ inline void softmax_row(float z[EPL]) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; i++) {
-    z[i] = expf(z[i] - m0);
+    z[i] = exp_neg(z[i] - m0);
     sum += z[i];
   }
   sum = wave_sum(sum);
@@ -45,10 +45,12 @@ __device__ inline void load_row(const float* row, int E, float z[EPL]) {
   for (int i = 0; i < EPL; i++) z[i] = lane + 64 * i < E ? row[lane + 64 * i] : -INFINITY;
 }
 
-// A block's share of the tokens (WAVES waves, one token each at a time): the
-// probability sums in sum[e], e = threadIdx.x + WAVES * 64 * i, the counts in
-// hist, the kept tokens returned.  The next token's logits are loaded before
-// this one's are used.
+// A wave loads the logits of kAhead tokens before it works on them: the loads'
+// latency is what a short batch consists of.
+constexpr int kAhead = 4;
+
+// A block's share of the tokens (WAVES waves, a token per wave at a time): the
+// waves' probability sums in ps, the counts in hist, the kept tokens returned.
 template <int EPL, int WAVES>
 struct Share {
   float ps[WAVES][64 * EPL];
@@ -61,26 +63,33 @@ struct Share {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     for (int e = threadIdx.x; e < 64 * EPL; e += 64 * WAVES) hist[e] = 0;
     __syncthreads();
-    float acc[EPL], z[EPL], nz[EPL];
+    float acc[EPL], z[kAhead][EPL];
 #pragma unroll
     for (int i = 0; i < EPL; i++) acc[i] = 0.f;
     int n = 0;
     const int step = gridDim.x * WAVES;
-    int t = blockIdx.x * WAVES + wave;
-    if (t < T) load_row<EPL>(logits + (size_t)t * E, E, nz);
-    for (; t < T; t += step) {
+    for (int t0 = blockIdx.x * WAVES + wave; t0 < T; t0 += step * kAhead) {
+      int pick[kAhead];
+      bool keep[kAhead];
 #pragma unroll
-      for (int i = 0; i < EPL; i++) z[i] = nz[i];
-      if (t + step < T) load_row<EPL>(logits + (size_t)(t + step) * E, E, nz);
-      if (mask && mask[t] == 0) continue;  // the same for the whole wave
-      n++;
-      if (lane < k) {
-        const int e = ids[(size_t)t * k + lane];
-        if (e >= 0 && e < E) atomicAdd(&hist[e], 1);
+      for (int a = 0; a < kAhead; a++) {
+        const int t = t0 + a * step;
+        keep[a] = t < T && (!mask || mask[t] != 0);  // the same for the whole wave
+        pick[a] = -1;
+        if (t < T) {
+          load_row<EPL>(logits + (size_t)t * E, E, z[a]);
+          if (lane < k) pick[a] = ids[(size_t)t * k + lane];
+        }
       }
-      softmax_row<EPL>(z);
 #pragma unroll
-      for (int i = 0; i < EPL; i++) acc[i] += z[i];
+      for (int a = 0; a < kAhead; a++) {
+        if (!keep[a]) continue;
+        n++;
+        if (pick[a] >= 0 && pick[a] < E) atomicAdd(&hist[pick[a]], 1);
+        softmax_row<EPL>(z[a]);
+#pragma unroll
+        for (int i = 0; i < EPL; i++) acc[i] += z[a][i];
+      }
     }
 #pragma unroll
     for (int i = 0; i < EPL; i++) ps[wave][lane + 64 * i] = acc[i];
@@ -127,59 +136,58 @@ __global__ __launch_bounds__(64 * kWaves) void balance_partial_kernel(
   }
 }
 
-// Adds the partials of nb blocks: a block sums 64 experts, each of its 16
-// waves every 16th partial; the last block to arrive forms the loss from the
+// Adds the partials of nb blocks: a block sums 32 experts, 32 threads each
+// over every 32nd partial; the last block to arrive forms the loss from the
 // blocks' terms, in order.
+constexpr int kFinish = 32;
 __global__ __launch_bounds__(1024) void balance_finish_kernel(BalanceParts w, int nb, int E, int k,
                                                               float coef, float* __restrict__ loss,
                                                               int32_t* __restrict__ counts,
                                                               float* __restrict__ probs,
                                                               int32_t* __restrict__ tokens) {
-  __shared__ double ps[16][64], sums[16];
-  __shared__ int cs[16][64], last;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int e = blockIdx.x * 64 + lane;
-  const int n = (int)block_sum64<16>((int)threadIdx.x < nb ? (double)w.nsum[threadIdx.x] : 0.0, sums);
+  __shared__ double ps[32][kFinish], sums[16];
+  __shared__ int cs[32][kFinish];
+  const int col = threadIdx.x % kFinish, group = threadIdx.x / kFinish;
+  const int e = blockIdx.x * kFinish + col;
   double p = 0.0;
   int c = 0;
   if (e < E) {
 #pragma unroll 8
-    for (int b = wave; b < nb; b += 16) {
+    for (int b = group; b < nb; b += 32) {
       p += (double)w.psum[(size_t)b * E + e];
       c += w.csum[(size_t)b * E + e];
     }
   }
-  ps[wave][lane] = p;
-  cs[wave][lane] = c;
-  __syncthreads();
-  if (wave == 0) {
+  ps[group][col] = p;
+  cs[group][col] = c;
+  const double kept = (int)threadIdx.x < nb ? (double)w.nsum[threadIdx.x] : 0.0;
+  const int n = (int)block_sum64<16>(kept, sums);  // with barriers before the reads below
+  if (threadIdx.x >= 64) return;
+  double term = 0.0;
+  if (group == 0) {
 #pragma unroll
-    for (int v = 1; v < 16; v++) {
-      p += ps[v][lane];
-      c += cs[v][lane];
+    for (int v = 1; v < 32; v++) {
+      p += ps[v][col];
+      c += cs[v][col];
     }
     p = n > 0 ? p / n : 0.0;
-    double term = 0.0;
     if (e < E) {
       counts[e] = c;
       probs[e] = (float)p;
       if (n > 0) term = (double)c / ((double)k * n) * p;
     }
-    term = wave_sum64(term);
-    if (lane == 0) {
-      w.terms[blockIdx.x] = term;
-      __threadfence();
-      last = atomicAdd(w.arrived, 1) == (int)gridDim.x - 1;
-      if (last) {
-        __threadfence();
-        double s = 0.0;
-        for (int b = 0; b < (int)gridDim.x; b++)
-          s += __hip_atomic_load(&w.terms[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        *loss = (float)((double)coef * E * s);
-        *tokens = n;
-      }
-    }
   }
+  term = wave_sum64(term);
+  if (threadIdx.x != 0) return;
+  w.terms[blockIdx.x] = term;
+  __threadfence();
+  if (atomicAdd(w.arrived, 1) != (int)gridDim.x - 1) return;
+  __threadfence();
+  double s = 0.0;
+  for (int b = 0; b < (int)gridDim.x; b++)
+    s += __hip_atomic_load(&w.terms[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  *loss = (float)((double)coef * E * s);
+  *tokens = n;
 }
 
 // Small batches in one launch of one block.
@@ -226,7 +234,6 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(
   for (int i = 0; i < EPL; i++)
     f[i] = lane + 64 * i < E ? (float)counts[lane + 64 * i] * kn : 0.f;
   for (int t = blockIdx.x * 4 + wave; t < T; t += gridDim.x * 4) {
-    float* out = dlogits + (size_t)t * E;
     float z[EPL];
     if (mask && mask[t] == 0) {
 #pragma unroll
@@ -241,6 +248,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(
 #pragma unroll
       for (int i = 0; i < EPL; i++) z[i] = g * z[i] * (f[i] - dot);
     }
+    float* out = dlogits + (size_t)t * E;
 #pragma unroll
     for (int i = 0; i < EPL; i++)
       if (lane + 64 * i < E) out[lane + 64 * i] = z[i];
@@ -283,8 +291,8 @@ hipError_t launch_balance(const float* logits, const int32_t* ids, const uint8_t
 #undef QMOE_CALL
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(balance_finish_kernel, dim3((E + 63) / 64), dim3(1024), 0, s, w, nb, E, k,
-                     coef, loss, counts, probs, tokens);
+  hipLaunchKernelGGL(balance_finish_kernel, dim3((E + kFinish - 1) / kFinish), dim3(1024), 0, s,
+                     w, nb, E, k, coef, loss, counts, probs, tokens);
   return hipGetLastError();
 }
 
@@ -292,6 +300,8 @@ hipError_t launch_balance_backward(const float* logits, const uint8_t* mask,
                                    const int32_t* counts, const int32_t* tokens,
                                    const float* dloss, int T, int E, int k, float coef,
                                    float* dlogits, hipStream_t s) {
+  // A token per wave up to 8192 of them: many waves hide the loads better than
+  // several tokens per wave do (8192 x 512: 11 against 14 us).
   const int nb = T < 4 * 2048 ? (T + 3) / 4 : 2048;
 #define QMOE_CALL(EPL)                                                                        \
   hipLaunchKernelGGL(balance_backward_kernel<EPL>, dim3(nb), dim3(256), 0, s, logits, mask,    \

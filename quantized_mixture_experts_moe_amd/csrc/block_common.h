@@ -140,11 +140,25 @@ __device__ inline float wave_fmax(float x) {
               __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 16 * row)));
   return r;
 }
-// Sum of doubles over the 64 lanes, the same in every lane.
+// Sum of doubles over the 64 lanes, the same in every lane (a fixed order).
+template <int CTRL>
+__device__ inline double dpp64(double x) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, x);
+  const unsigned long long lo = dpp<CTRL>((uint32_t)b), hi = dpp<CTRL>((uint32_t)(b >> 32));
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
+__device__ inline double readlane64(double x, int lane) {
+  const unsigned long long b = __builtin_bit_cast(unsigned long long, x);
+  const unsigned long long lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, lane);
+  const unsigned long long hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, hi << 32 | lo);
+}
 __device__ inline double wave_sum64(double x) {
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) x += __shfl_xor(x, off, 64);
-  return x;
+  x += dpp64<0xB1>(x);
+  x += dpp64<0x4E>(x);
+  x += dpp64<0x141>(x);
+  x += dpp64<0x140>(x);
+  return (readlane64(x, 0) + readlane64(x, 16)) + (readlane64(x, 32) + readlane64(x, 48));
 }
 
 __device__ inline uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
@@ -170,17 +184,47 @@ struct Quant {
     r = 1.0f / s;
     bad = amax >= 0x7f800000u;
   }
+  // No clamp: a quotient is at most 448 (1 + 2^-24) in size, which rounds to
+  // 448 (the next step up would begin at 464).
   __device__ inline uint32_t e4m3x4(float a, float b, float c, float d) const {
-    return bad ? 0u : rq::quant4<true>(a, b, c, d, s, r, refine);
+    if (bad) return 0u;
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(rq::quotient(a, s, r, refine),
+                                            rq::quotient(b, s, r, refine), 0, false);
+    v = __builtin_amdgcn_cvt_pk_fp8_f32(rq::quotient(c, s, r, refine),
+                                        rq::quotient(d, s, r, refine), v, true);
+    return (uint32_t)v;
   }
   __device__ inline uint32_t i8x4(float a, float b, float c, float d) const {
     return bad ? 0u : rq::quant4<false>(a, b, c, d, s, r, refine);
   }
 };
 
-// SiLU(g) * u with the library exponential and an IEEE division: the codes
-// that follow are decided in fp32.
-__device__ inline float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// e^x for x <= 0 (0 for -inf, NaN for NaN), within two units in the last
+// place: the argument of the hardware's power of two in two parts, as below.
+__device__ inline float exp_neg(float x) {
+  const float hi = x * 1.44269502162933349609375f;
+  const float lo = __builtin_fmaf(x, 1.44269502162933349609375f, -hi) + x * 1.925963033500e-8f;
+  const float e = __builtin_amdgcn_exp2f(hi);
+  return hi < -150.0f ? 0.0f : __builtin_fmaf(e, lo * 0.693147180559945f, e);
+}
+
+// SiLU(g) * u = g / (1 + 2^(-g log2 e)) * u, a few units in the last place
+// off: the exponent's argument in two parts (the product with log2 e rounded,
+// and what the rounding and the constant's own tail leave, which enters as a
+// factor 1 + tail ln 2), the hardware's power of two, and its reciprocal
+// improved by one Newton step.  (The library's exponential and an IEEE
+// division cost twice the instructions, and the quantizer's time is these.)
+__device__ inline float silu_mul(float g, float u) {
+  const float hi = g * -1.44269502162933349609375f;
+  const float lo = __builtin_fmaf(g, -1.44269502162933349609375f, -hi) - g * 1.925963033500e-8f;
+  float e = __builtin_amdgcn_exp2f(hi);
+  e = __builtin_fmaf(e, lo * 0.693147180559945f, e);
+  const float d = 1.0f + e;
+  float r = __builtin_amdgcn_rcpf(d);
+  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  // A power that overflows: SiLU is -0, and the step above has no meaning.
+  return (hi >= 126.0f ? g * 0.0f : g * r) * u;
+}
 
 }  // namespace bk
 }  // namespace qmoe

@@ -50,7 +50,7 @@ hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s);
 hipError_t launch_fp8_grouped_matmul(const Fp8MatmulArgs& g, hipStream_t s);
 
 // Workspace of the balance loss: per block (balance_blocks) the probability
-// sums and counts [E] and kept tokens; per 64 experts a term of the loss; the
+// sums and counts [E] and kept tokens; per 32 experts a term of the loss; the
 // blocks that have arrived.  A small batch needs none.
 struct BalanceParts {
   float* psum;

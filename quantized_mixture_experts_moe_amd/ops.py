@@ -580,12 +580,16 @@ def fp8_quant(x: torch.Tensor, block: bool = False, act: Optional[str] = None, r
 
 def _operand(codes, scale, name: str, block: bool, lead=()):
     """Checks codes [.., rows, K] with their scales; returns (rows, K)."""
-    _need(codes.dim() == 2 + len(lead), "%s must have %d axes", name, 2 + len(lead))
-    n, k = codes.shape[-2:]
+    shape = codes.shape
+    _need(len(shape) == 2 + len(lead), "%s must have %d axes", name, 2 + len(lead))
+    n, k = shape[-2], shape[-1]
     _need(k >= 128 and k % 128 == 0, "%s's row length %d is not a multiple of 128", name, k)
-    _tensor(codes, name, lead + (n, k), torch.uint8)
-    _tensor(scale, f"{name}_scale", lead + ((_blocks(n), k // 128) if block else (k // 128, n)),
-            torch.float32)
+    kb = k // 128
+    want = lead + (((n + 127) // 128, kb) if block else (kb, n))
+    if (scale.shape != want or codes.dtype != torch.uint8 or scale.dtype != torch.float32
+            or shape[:-2] != lead):
+        _tensor(codes, name, lead + (n, k), torch.uint8)
+        _tensor(scale, f"{name}_scale", want, torch.float32)
     return n, k
 
 
