@@ -18,9 +18,13 @@ using namespace bk;
 
 // Softmax of one row held as z[EPL] (expert e = lane + 64 i; missing experts
 // hold -inf): p in place.  A row of -inf alone (every expert masked) has no
-// softmax and gives zeros; a NaN or +inf gives NaN.
+// softmax and gives zeros; a NaN or +inf gives NaN.  The difference to the
+// maximum comes first (logits down to the lowest finite number are masks too),
+// then its product with log2 e: two roundings of z - max in the exponent, which
+// are small where p is not.
 template <int EPL>
 __device__ inline void softmax_row(float z[EPL]) {
+  constexpr float kLog2e = 1.44269502162933349609375f;
   float mx = z[0];
 #pragma unroll
   for (int i = 1; i < EPL; i++) mx = fmaxf(mx, z[i]);
@@ -29,7 +33,7 @@ __device__ inline void softmax_row(float z[EPL]) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; i++) {
-    z[i] = exp_neg(z[i] - m0);
+    z[i] = __builtin_amdgcn_exp2f((z[i] - m0) * kLog2e);
     sum += z[i];
   }
   sum = wave_sum(sum);

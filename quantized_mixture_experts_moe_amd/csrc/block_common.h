@@ -199,15 +199,6 @@ struct Quant {
   }
 };
 
-// e^x for x <= 0 (0 for -inf, NaN for NaN), within two units in the last
-// place: the argument of the hardware's power of two in two parts, as below.
-__device__ inline float exp_neg(float x) {
-  const float hi = x * 1.44269502162933349609375f;
-  const float lo = __builtin_fmaf(x, 1.44269502162933349609375f, -hi) + x * 1.925963033500e-8f;
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return hi < -150.0f ? 0.0f : __builtin_fmaf(e, lo * 0.693147180559945f, e);
-}
-
 // SiLU(g) * u = g / (1 + 2^(-g log2 e)) * u, a few units in the last place
 // off: the exponent's argument in two parts (the product with log2 e rounded,
 // and what the rounding and the constant's own tail leave, which enters as a

@@ -501,30 +501,30 @@ def _addr(t):
     """A tensor's address (None for one left out)."""
     if t is None:
         return None
-    if not t.is_contiguous():
-        raise ValueError("tensors passed to libqmoe must be contiguous")
-    return t.data_ptr()
+    if t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("tensors passed to libqmoe must be contiguous")
 
 
-def _raw_stream(dev) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
-# The same look-up without a Stream object (0.1 against 1.9 us), where this
-# torch has it.
-_raw_stream_by_index = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and its stream without Python objects in between (0.1
+# against 1.9 us), where this torch has the calls.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call(dev, name: str, *args):
     """The library call `name` with the device current (a launch goes to the
     current device's context) and its current stream as the last argument."""
-    fn = getattr(_lib(), name)
-    stream = _raw_stream(dev) if _raw_stream_by_index is None else _raw_stream_by_index(dev.index)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, stream)
+    index = dev.index
+    if _current_device() == index:
+        status = getattr(_LIB or _lib(), name)(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, stream)
+            status = getattr(_LIB or _lib(), name)(*args, _raw_stream(index))
     if status != QMOE_OK:
         raise QmoeError(status, name)
 
@@ -709,7 +709,7 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
          "probs": torch.empty(E, dtype=torch.float32, device=dev),
          "tokens": torch.empty(1, dtype=torch.int32, device=dev)}
     _call(dev, "qmoe_balance", _addr(logits), _addr(topk_ids), _mask_ptr(mask, T), T, E, k, coef,
-          _addr(r["loss"]), _addr(r["counts"]), _addr(r["probs"]), _addr(r["tokens"]), _addr(ws),
+          r["loss"].data_ptr(), r["counts"].data_ptr(), r["probs"].data_ptr(), r["tokens"].data_ptr(), _addr(ws),
           0 if ws is None else ws.numel() * ws.element_size())
     return r
 
@@ -772,7 +772,7 @@ def pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, out: str 
     _tensor(weight, "weight", (H,), torch.float32)
     dev = _one_device(x, weight)
     form, n, scale = _new_form(out, T, H, dev)
-    _call(dev, "qmoe_pre_norm", _addr(x), dt, _addr(weight), eps, T, H, form, _addr(n), _addr(scale))
+    _call(dev, "qmoe_pre_norm", _addr(x), dt, _addr(weight), eps, T, H, form, n.data_ptr(), _addr(scale))
     return n, scale
 
 
@@ -825,7 +825,7 @@ def pre_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, e
     dw = torch.empty(H, dtype=torch.float32, device=dev)
     ws, nbytes = _norm_ws(ws, H, dev)
     _call(dev, "qmoe_pre_norm_backward", _addr(dn), _addr(x), dt, _addr(weight), eps, _addr(dres), T,
-          H, _addr(dx), _addr(dw), _addr(ws), nbytes)
+          H, dx.data_ptr(), dw.data_ptr(), _addr(ws), nbytes)
     return dx, dw
 
 
@@ -847,6 +847,6 @@ def post_norm_backward(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor
          "dgate": None if gate is None else torch.empty_like(gate)}
     ws, nbytes = _norm_ws(ws, H, dev)
     _call(dev, "qmoe_post_norm_backward", _addr(dout), _addr(y), dt, _addr(weight), gp, kind, alpha,
-          eps, T, H, _addr(r["dy"]), _addr(r["dres"]), _addr(r["dw"]), _addr(r["dgate"]), _addr(ws),
+          eps, T, H, r["dy"].data_ptr(), r["dres"].data_ptr(), r["dw"].data_ptr(), _addr(r["dgate"]), _addr(ws),
           nbytes)
     return r
