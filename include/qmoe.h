@@ -366,7 +366,7 @@ qmoe_status qmoe_decode(const qmoe_ffn_desc* d, const float* logits, const void*
  *   Kp and Mp are K and M rounded up to a multiple of 128; codes behind K
  *   (behind M in codes_t) are written as 0.
  * Either pair may be NULL, not both.  codes, codes_t: 16-byte aligned.
- * Limits: B <= 65535, M <= 65535 * 128, K <= 2^30 (QMOE_ERR_UNSUPPORTED). */
+ * Limits: B <= 65535, M <= 65535 * 128, K <= 2^29 (QMOE_ERR_UNSUPPORTED). */
 qmoe_status qmoe_fp8_quant(const void* x, int32_t dtype, int32_t B, int32_t M, int32_t K,
                            int32_t block, int32_t act, uint8_t* codes, float* scale,
                            uint8_t* codes_t, float* scale_t, void* stream);
@@ -430,7 +430,7 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
  *   has probability 0; a row of -inf alone has probability 0 everywhere (it
  *   is still a kept token); NaN or +inf in a kept row makes the loss NaN.
  * logits fp32 [T,E]; topk_ids int32 [T,k]; loss fp32 [1], counts int32 [E],
- *   probs fp32 [E], tokens int32 [1].  k <= 16, E <= 1024.
+ *   probs fp32 [E], tokens int32 [1].  k <= 16, E <= 1024, T*k <= 2^30.
  * ws: qmoe_balance_workspace(T, E) bytes (0 for a small batch: ws may be
  *   NULL), 256-byte aligned, contents need no initialisation; calls that
  *   share it must be ordered on one stream.

@@ -64,7 +64,7 @@ qmoe_status qmoe_fp8_quant(const void* x, int32_t dtype, int32_t B, int32_t M, i
   if ((!block && B > 1) || (block && act)) return QMOE_ERR_INVALID_ARG;
   if ((codes == nullptr) != (scale == nullptr) || (codes_t == nullptr) != (scale_t == nullptr))
     return QMOE_ERR_INVALID_ARG;
-  if (B > 65535 || M > 65535 * 128 || K > (1 << 30)) return QMOE_ERR_UNSUPPORTED;
+  if (B > 65535 || M > 65535 * 128 || K > (1 << 29)) return QMOE_ERR_UNSUPPORTED;
   if (B == 0 || M == 0) return QMOE_OK;
   if (x == nullptr || (codes == nullptr && codes_t == nullptr)) return QMOE_ERR_INVALID_ARG;
   if (!aligned(x, elem(dtype)) || !aligned(codes, 16) || !aligned(codes_t, 16) ||
@@ -108,7 +108,6 @@ qmoe_status qmoe_fp8_matmul(const uint8_t* a, const float* a_scale, const uint8_
   g.b_block = b_block != 0;
   g.out_f32 = out_dtype == QMOE_DT_F32;
   g.parts = reinterpret_cast<float*>(ws);
-  g.parts_bytes = need;
   return hip_status(launch_fp8_matmul(g, (hipStream_t)stream));
 }
 
@@ -172,6 +171,7 @@ qmoe_status qmoe_balance(const float* logits, const int32_t* topk_ids, const uin
                          size_t ws_bytes, void* stream) {
   if (T < 0 || E < 1 || k < 1 || k > E || k > 16 || !std::isfinite(coef))
     return QMOE_ERR_INVALID_ARG;
+  if ((long long)T * k > (1ll << 30)) return QMOE_ERR_INVALID_ARG;
   if (E > 1024) return QMOE_ERR_UNSUPPORTED;
   if ((T > 0 && (!logits || !topk_ids)) || !loss || !counts || !probs || !tokens)
     return QMOE_ERR_INVALID_ARG;
@@ -193,6 +193,7 @@ qmoe_status qmoe_balance_backward(const float* logits, const uint8_t* mask, cons
                                   int32_t k, float coef, float* dlogits, void* stream) {
   if (T < 0 || E < 1 || k < 1 || k > E || k > 16 || !std::isfinite(coef))
     return QMOE_ERR_INVALID_ARG;
+  if ((long long)T * k > (1ll << 30)) return QMOE_ERR_INVALID_ARG;
   if (E > 1024) return QMOE_ERR_UNSUPPORTED;
   if (T == 0) return QMOE_OK;
   if (!logits || !counts || !tokens || !dloss || !dlogits) return QMOE_ERR_INVALID_ARG;

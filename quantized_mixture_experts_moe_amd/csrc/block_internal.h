@@ -42,7 +42,6 @@ struct Fp8MatmulArgs {
   bool pair_rows;
   // dense: sums of a K split in parts [splits, M, N] fp32
   float* parts;
-  size_t parts_bytes;
   int split_kb;  // K blocks per part (set by the launcher)
 };
 size_t fp8_matmul_parts_bytes(int M, int N, int K);

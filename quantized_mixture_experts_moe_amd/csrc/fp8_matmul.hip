@@ -258,10 +258,6 @@ __device__ inline void copy4(Rsrc r, unsigned voff, float* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
                                            (int)voff, 0, 0, 0);
 }
-__device__ inline float load_f32(Rsrc r, unsigned voff) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)voff, 0, 0));
-}
-
 // Waits until at most N of the wave's memory operations are under way (they
 // end in order; a barrier alone does not wait for copies to LDS).
 template <int N>
@@ -376,14 +372,15 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void fp8_matmul_tile_kernel(Fp8M
   auto out_row = [&](int slot) {
     return GROUPED && slot >= mend ? -1 : Rows<GROUPED>::out_row(g, slot);
   };
-  // The wave's sub-tiles of rows are wm, wm + WM, ...; those with rows come
-  // first (an expert's rows stand in front of its padding).
+  // The wave's sub-tiles of rows are wm, wm + WM, ...; those behind the last
+  // one with a row (an expert's rows stand in front of its padding) are left
+  // out.
   int live = SM;
   if constexpr (GROUPED) {
     live = 0;
 #pragma unroll
     for (int s = 0; s < SM; s++)
-      live += out_row(m0 + (s * C::WM + wm) * 32) >= 0;
+      if (__ballot(out_row(m0 + (s * C::WM + wm) * 32 + (lane & 31)) >= 0) != 0) live = s + 1;
     live = __builtin_amdgcn_readfirstlane(live);
   }
   // Copies: 8 lanes per row, the rows of a wave's copy t being 8 t .. 8 t + 7.
@@ -698,36 +695,36 @@ __global__ __launch_bounds__(256) void fp8_matmul_sum_kernel(const float* __rest
   }
 }
 
-template <class C, bool GROUPED, bool BBLOCK, bool EXACT>
-hipError_t launch_tile(Fp8MatmulArgs g, int splits, hipStream_t s) {
+// Tiles of a product; `splits` parts of K with fp32 outputs (OUT32).
+template <class C, bool GROUPED, bool BBLOCK, bool EXACT, bool OUT32 = EXACT>
+hipError_t launch_tile(Fp8MatmulArgs g, hipStream_t s, int splits = 1) {
   // Grouped: at most one row tile per BM rows and one more per expert.
   const long long ntm = GROUPED ? g.M / C::BM + (g.E < g.P ? g.E : g.P) : (g.M + C::BM - 1) / C::BM;
   const long long total = (long long)((g.N + C::BN - 1) / C::BN) * ntm;
   if (total > (1ll << 30)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((total + 7) / 8 * 8), splits), block(C::THREADS);
   g.split_kb = (g.KB + splits - 1) / splits;
-  if constexpr (!GROUPED) {
-    if (splits > 1) {
-      void* out = g.out;
-      g.out = g.parts;
-      hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, false, BBLOCK, EXACT, true>), grid, block, 0,
-                         s, g);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-      const size_t count = (size_t)g.M * g.N;
-      const bool wide = count % 4 == 0 && (uintptr_t)out % 16 == 0;
-      const dim3 sg((unsigned)((count + 1023) / 1024));
-      if (g.out_f32)
-        hipLaunchKernelGGL(fp8_matmul_sum_kernel<true>, sg, dim3(256), 0, s, g.parts, splits,
-                           count, out, wide);
-      else
-        hipLaunchKernelGGL(fp8_matmul_sum_kernel<false>, sg, dim3(256), 0, s, g.parts, splits,
-                           count, out, wide);
-      return hipGetLastError();
-    }
-  }
-  hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, EXACT, EXACT>), grid, block, 0, s,
-                     g);
+  hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, EXACT, OUT32>),
+                     dim3((unsigned)((total + 7) / 8 * 8), splits), dim3(C::THREADS), 0, s, g);
+  return hipGetLastError();
+}
+
+// A product whose K is split: the parts' sums in g.parts, then their total.
+template <class C, bool BBLOCK, bool EXACT>
+hipError_t launch_split(Fp8MatmulArgs g, int splits, hipStream_t s) {
+  if (splits == 1) return launch_tile<C, false, BBLOCK, EXACT>(g, s);
+  void* out = g.out;
+  g.out = g.parts;
+  const hipError_t e = launch_tile<C, false, BBLOCK, EXACT, true>(g, s, splits);
+  if (e != hipSuccess) return e;
+  const size_t count = (size_t)g.M * g.N;
+  const bool wide = count % 4 == 0 && (uintptr_t)out % 16 == 0;
+  const dim3 grid((unsigned)((count + 1023) / 1024));
+  if (g.out_f32)
+    hipLaunchKernelGGL(fp8_matmul_sum_kernel<true>, grid, dim3(256), 0, s, g.parts, splits, count,
+                       out, wide);
+  else
+    hipLaunchKernelGGL(fp8_matmul_sum_kernel<false>, grid, dim3(256), 0, s, g.parts, splits, count,
+                       out, wide);
   return hipGetLastError();
 }
 
@@ -788,15 +785,15 @@ hipError_t dense(const Fp8MatmulArgs& g, hipStream_t s) {
   // (Big is built for the products that reach its size: weights, bf16.)
   const Plan p = plan(g.M, g.N, g.K, BBLOCK && !EXACT);
   if constexpr (BBLOCK && !EXACT) {
-    if (p.kernel == kBig) return launch_tile<Big, false, true, false>(g, p.splits, s);
+    if (p.kernel == kBig) return launch_tile<Big, false, true, false>(g, s);
   }
   switch (p.kernel) {
     case kRows:
       return g.M <= 16 ? launch_rows<1, false, BBLOCK, EXACT>(g, s)
                        : launch_rows<2, false, BBLOCK, EXACT>(g, s);
-    case kSmall: return launch_tile<Small, false, BBLOCK, EXACT>(g, p.splits, s);
-    case kHalf: return launch_tile<Half, false, BBLOCK, EXACT>(g, p.splits, s);
-    default: return launch_tile<Mid, false, BBLOCK, EXACT>(g, p.splits, s);
+    case kSmall: return launch_split<Small, BBLOCK, EXACT>(g, p.splits, s);
+    case kHalf: return launch_tile<Half, false, BBLOCK, EXACT>(g, s);
+    default: return launch_tile<Mid, false, BBLOCK, EXACT>(g, s);
   }
 }
 
@@ -818,14 +815,14 @@ hipError_t grouped(const Fp8MatmulArgs& g, hipStream_t s) {
     return ((double)g.P / bm + (g.E < g.P ? g.E : g.P) * 0.5) * ((g.N + bn - 1) / bn);
   };
   if constexpr (EXACT) {  // (its sums of a K block need the registers of a smaller tile)
-    if (mean > 48 && blocks(128, 128) >= 2 * cus) return launch_tile<Mid, true, true, true>(g, 1, s);
+    if (mean > 48 && blocks(128, 128) >= 2 * cus) return launch_tile<Mid, true, true, true>(g, s);
   } else {
-    if (mean > 96 && blocks(256, 256) >= 2 * cus) return launch_tile<Big, true, true, false>(g, 1, s);
-    if (mean > 48 && blocks(128, 256) >= 2 * cus) return launch_tile<Wide, true, true, false>(g, 1, s);
+    if (mean > 96 && blocks(256, 256) >= 2 * cus) return launch_tile<Big, true, true, false>(g, s);
+    if (mean > 48 && blocks(128, 256) >= 2 * cus) return launch_tile<Wide, true, true, false>(g, s);
   }
-  if (mean > 20 && blocks(64, 128) >= cus) return launch_tile<Half, true, true, EXACT>(g, 1, s);
-  return blocks(32, 128) >= 2 * cus ? launch_tile<Low, true, true, EXACT>(g, 1, s)
-                                    : launch_tile<LowFew, true, true, EXACT>(g, 1, s);
+  if (mean > 20 && blocks(64, 128) >= cus) return launch_tile<Half, true, true, EXACT>(g, s);
+  return blocks(32, 128) >= 2 * cus ? launch_tile<Low, true, true, EXACT>(g, s)
+                                    : launch_tile<LowFew, true, true, EXACT>(g, s);
 }
 }  // namespace
 

@@ -37,7 +37,7 @@ def test_fp8_quant_refusals():
                 dict(scale=ctypes.c_void_p(0x10002))):
         assert c(**bad) == INV, bad
     assert c(block=1, B=70000) == UNS
-    assert c(M=65535 * 128 + 1) == UNS
+    assert c(M=65535 * 128 + 1) == UNS and c(K=(1 << 29) + 1) == UNS
     assert c(M=0, x=None) == OK and c(B=0, x=None) == OK
 
 
@@ -83,7 +83,7 @@ def test_balance_refusals():
     assert n >= 256 and n % 256 == 0 and ws(-1, 8) == 0 and ws(4, 0) == 0
     c = _caller("qmoe_balance", logits=P, ids=P, mask=None, T=6400, E=8, k=2, coef=0.1, loss=P,
                 counts=P, probs=P, tokens=P, ws=P, ws_bytes=n, stream=None)
-    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(E=64, k=17), dict(coef=NAN),
+    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(E=64, k=17), dict(T=(1 << 29) + 1), dict(coef=NAN),
                 dict(coef=INF), dict(logits=None), dict(ids=None), dict(loss=None),
                 dict(counts=None), dict(probs=None), dict(tokens=None), dict(ws=None),
                 dict(ws_bytes=n - 1), dict(ws=ODD)):
@@ -91,8 +91,8 @@ def test_balance_refusals():
     assert c(E=1025, ws_bytes=1 << 40) == UNS
     b = _caller("qmoe_balance_backward", logits=P, mask=None, counts=P, tokens=P, dloss=P, T=64,
                 E=8, k=2, coef=0.1, dlogits=P, stream=None)
-    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(coef=INF), dict(logits=None),
-                dict(counts=None), dict(tokens=None), dict(dloss=None), dict(dlogits=None)):
+    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(T=(1 << 29) + 1), dict(coef=INF),
+                dict(logits=None), dict(counts=None), dict(tokens=None), dict(dloss=None), dict(dlogits=None)):
         assert b(**bad) == INV, bad
     assert b(E=1025) == UNS
     assert b(T=0, logits=None) == OK

@@ -331,6 +331,55 @@ def test_grouped_matmul_one_expert_takes_all_and_dropped_pairs_stay(bm):
     assert (out[14:16] == 11).all()
 
 
+@pytest.mark.parametrize("T", [20, 90, 400, 900])
+def test_grouped_matmul_with_holes_in_the_list(T):
+    """Slots of the expert-sorted list that hold no pair, in front of, between
+    and behind others (what an id repeated within a token leaves)."""
+    E, k, N, K, bm = 3, 1, 300, 256, 16
+    ids, al, b, sb = _grouped_case(T, E, k, N, K, bm, seed=T)
+    q = ops.fp8_quant(_rand(T, K, seed=8))
+    srt, first = al["sorted_pair_ids"], al["expert_offsets"].tolist()
+    gone = []
+    for e in range(E):
+        for at in list(range(0, 40)) + [64, 96, 127, 128, 160]:
+            slot = first[e] + at
+            if slot < first[e + 1] and int(srt[slot]) < T and at % 3 != 1:
+                gone.append(int(srt[slot]))
+                srt[slot] = T * k
+    out = torch.full((T, N), 5.0, dtype=BF, device="cuda")
+    ops.fp8_grouped_matmul(q["codes"], q["scale"], b, sb, al, k, out=out)
+    there = torch.ones(T, dtype=torch.bool, device="cuda")
+    there[gone] = False
+    assert (out[gone] == 5).all()
+    ids2 = ids.clone()
+    ids2[gone] = -1
+    _grouped_check(out, ids2, q["codes"], q["scale"], b, sb, k, False, K)
+
+
+@pytest.mark.parametrize("bm", [16, 64])
+def test_grouped_matmul_over_many_experts_skewed(bm):
+    """1024 experts, most without a row, a few with hundreds."""
+    T, E, k, N, K = 600, 1024, 2, 160, 128
+    z = _rand(T, E, seed=2) - 2.5 * torch.log(torch.arange(1, E + 1, device="cuda").float())
+    ids = z.topk(k, 1).indices.to(torch.int32)
+    ids, al, b, sb = _grouped_case(T, E, k, N, K, bm, ids=ids)
+    q = ops.fp8_quant(_rand(T, K, seed=3))
+    out = torch.full((T * k, N), float("nan"), dtype=BF, device="cuda")
+    ops.fp8_grouped_matmul(q["codes"], q["scale"], b, sb, al, k, out=out)
+    _grouped_check(out, ids, q["codes"], q["scale"], b, sb, k, False, K)
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(1200, 4, 2, 1100, 256), (3000, 8, 2, 2100, 128),
+                                       (900, 64, 4, 1030, 128), (500, 60, 8, 1500, 256)])
+def test_grouped_matmul_large_tiles(T, E, k, N, K):
+    ids, al, b, sb = _grouped_case(T, E, k, N, K, ops.fp8_block_m(T, k, E), seed=T)
+    q = ops.fp8_quant(_rand(T, K, seed=3))
+    for dt in (BF, F32):
+        out = torch.full((T * k, N), float("nan"), dtype=dt, device="cuda")
+        ops.fp8_grouped_matmul(q["codes"], q["scale"], b, sb, al, k, out=out, out_dtype=dt)
+        _grouped_check(out, ids, q["codes"], q["scale"], b, sb, k, False, K)
+
+
 def test_grouped_matmul_refuses_what_does_not_fit():
     ids, al, b, sb = _grouped_case(20, 4, 2, 64, 128, 16)
     q = ops.fp8_quant(_rand(20, 128))

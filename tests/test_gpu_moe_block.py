@@ -75,6 +75,14 @@ def test_block(T, H, I, E, k):
     assert torch.equal(n, r["next"]) and torch.equal(s, r["next_scale"])
 
 
+def test_block_of_no_tokens():
+    b = Block(256, 128, 8, 2)
+    x, logits = _rand(0, 256, dtype=BF), _rand(0, 8)
+    r = b(x, logits)
+    assert r["out"].shape == (0, 256) and r["next"].shape == (0, 256) and r["dz"].shape == (0, 8)
+    assert float(r["loss"]) == 0 and not r["counts"].any()
+
+
 @pytest.mark.parametrize("T", [1, 48, 400])
 def test_block_in_a_graph_and_on_a_stream(T):
     """Captured once, replayed on new inputs between eager calls, against the
