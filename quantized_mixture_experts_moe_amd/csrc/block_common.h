@@ -114,17 +114,16 @@ __device__ inline uint32_t wave_max(uint32_t x) {
     r = max(r, (uint32_t)__builtin_amdgcn_readlane((int)x, 16 * row));
   return r;
 }
+__device__ inline float readlane(float x, int lane) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), lane));
+}
 // Sum over the 64 lanes, the same in every lane (a fixed order).
 __device__ inline float wave_sum(float x) {
   x += __uint_as_float(dpp<0xB1>(__float_as_uint(x)));
   x += __uint_as_float(dpp<0x4E>(__float_as_uint(x)));
   x += __uint_as_float(dpp<0x141>(__float_as_uint(x)));
   x += __uint_as_float(dpp<0x140>(__float_as_uint(x)));
-  float r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 0));
-#pragma unroll
-  for (int row = 1; row < 4; row++)
-    r += __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 16 * row));
-  return r;
+  return (readlane(x, 0) + readlane(x, 16)) + (readlane(x, 32) + readlane(x, 48));
 }
 
 // Maximum over the 64 lanes (NaN lanes are passed over), in every lane.
@@ -133,12 +132,7 @@ __device__ inline float wave_fmax(float x) {
   x = fmaxf(x, __uint_as_float(dpp<0x4E>(__float_as_uint(x))));
   x = fmaxf(x, __uint_as_float(dpp<0x141>(__float_as_uint(x))));
   x = fmaxf(x, __uint_as_float(dpp<0x140>(__float_as_uint(x))));
-  float r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 0));
-#pragma unroll
-  for (int row = 1; row < 4; row++)
-    r = fmaxf(r,
-              __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 16 * row)));
-  return r;
+  return fmaxf(fmaxf(readlane(x, 0), readlane(x, 16)), fmaxf(readlane(x, 32), readlane(x, 48)));
 }
 // Sum of doubles over the 64 lanes, the same in every lane (a fixed order).
 template <int CTRL>

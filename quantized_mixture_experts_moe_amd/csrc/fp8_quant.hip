@@ -177,15 +177,16 @@ hipError_t launch(const Fp8QuantArgs& a, hipStream_t s) {
   if (a.block) {
     if constexpr (!ACT) {
       hipLaunchKernelGGL((fp8_quant_tile_kernel<F32, false, true>), dim3(KB, MB, a.B),
-                         dim3(kTileThreads), 0, s, a.x, a.M, a.K, KB, MB, vec, a.codes, a.scale, a.codes_t,
-                         a.scale_t);
+                         dim3(kTileThreads), 0, s, a.x, a.M, a.K, KB, MB, vec, a.codes, a.scale,
+                         a.codes_t, a.scale_t);
       return hipGetLastError();
     }
     return hipErrorInvalidValue;
   }
   if (a.codes_t) {
-    hipLaunchKernelGGL((fp8_quant_tile_kernel<F32, ACT, false>), dim3(KB, MB, 1), dim3(kTileThreads), 0, s,
-                       a.x, a.M, a.K, KB, MB, vec, a.codes, a.scale, a.codes_t, a.scale_t);
+    hipLaunchKernelGGL((fp8_quant_tile_kernel<F32, ACT, false>), dim3(KB, MB, 1),
+                       dim3(kTileThreads), 0, s, a.x, a.M, a.K, KB, MB, vec, a.codes, a.scale,
+                       a.codes_t, a.scale_t);
     return hipGetLastError();
   }
   const int mb = (a.M + 15) / 16;

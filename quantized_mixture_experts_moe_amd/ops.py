@@ -618,8 +618,8 @@ def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale:
     need = fp8_matmul_workspace(M, N, K)
     if ws is None or ws.numel() * ws.element_size() < need:
         ws = _ws(need, dev) if need else None
-    _call(dev, "qmoe_fp8_matmul", _addr(a), _addr(a_scale), _addr(b), _addr(b_scale), int(b_block), M,
-          N, K, _addr(out), _float_kind(out, "out"), _addr(ws),
+    _call(dev, "qmoe_fp8_matmul", _addr(a), _addr(a_scale), _addr(b), _addr(b_scale),
+          int(b_block), M, N, K, _addr(out), _float_kind(out, "out"), _addr(ws),
           0 if ws is None else ws.numel() * ws.element_size())
     return out
 
@@ -651,15 +651,14 @@ def fp8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
     out = _out(out, (T * k, N), out_dtype, dev)
     _call(dev, "qmoe_fp8_grouped_matmul", _addr(a), _addr(a_scale), int(pair_rows), _addr(b),
           _addr(b_scale), _addr(al["sorted_pair_ids"]), _addr(al["tile_expert"]),
-          _addr(al["expert_offsets"]), _addr(al["num_padded"]), T, k, E, bm, N, K, _addr(out), _float_kind(out, "out"))
+          _addr(al["expert_offsets"]), _addr(al["num_padded"]), T, k, E, bm, N, K, _addr(out),
+          _float_kind(out, "out"))
     return out
 
 
-def fp8_block_m(T: int, k: int, E: int) -> int:
-    """Tile height (align's block_m) for the block-128 fp8 expert products:
-    the smallest that holds the mean rows per expert."""
-    mean = T * k / E
-    return 16 if mean <= 16 else 32 if mean <= 32 else 64 if mean <= 64 else 128
+# Tile height (align's block_m) for the block-128 fp8 expert products: they
+# take an expert's rows whatever the height, so the least padding is best.
+FP8_BLOCK_M = 16
 
 
 def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor, weights: dict,
@@ -671,9 +670,8 @@ def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor
     (fp8_quant(w, block=True)), H % 128 == 0, I % 128 == 0."""
     T, E = logits.shape
     _need(x.shape[0] == T, "x has %d rows, logits %d", x.shape[0], T)
-    block_m = fp8_block_m(T, k, E)
     with torch.cuda.device(_one_device(logits, x)):
-        ids, w, al = route_align(logits, k, block_m)
+        ids, w, al = route_align(logits, k, FP8_BLOCK_M)
         gu = fp8_grouped_matmul(x, x_scale, weights["w13"], weights["w13_scale"], al, k)
         h = fp8_quant(gu, act="silu_mul")
         y = fp8_grouped_matmul(h["codes"], h["scale"], weights["w2"], weights["w2_scale"], al, k,
@@ -709,8 +707,8 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
          "probs": torch.empty(E, dtype=torch.float32, device=dev),
          "tokens": torch.empty(1, dtype=torch.int32, device=dev)}
     _call(dev, "qmoe_balance", _addr(logits), _addr(topk_ids), _mask_ptr(mask, T), T, E, k, coef,
-          r["loss"].data_ptr(), r["counts"].data_ptr(), r["probs"].data_ptr(), r["tokens"].data_ptr(), _addr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+          r["loss"].data_ptr(), r["counts"].data_ptr(), r["probs"].data_ptr(),
+          r["tokens"].data_ptr(), _addr(ws), 0 if ws is None else ws.numel() * ws.element_size())
     return r
 
 
@@ -772,7 +770,8 @@ def pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, out: str 
     _tensor(weight, "weight", (H,), torch.float32)
     dev = _one_device(x, weight)
     form, n, scale = _new_form(out, T, H, dev)
-    _call(dev, "qmoe_pre_norm", _addr(x), dt, _addr(weight), eps, T, H, form, n.data_ptr(), _addr(scale))
+    _call(dev, "qmoe_pre_norm", _addr(x), dt, _addr(weight), eps, T, H, form, n.data_ptr(),
+          _addr(scale))
     return n, scale
 
 
@@ -824,8 +823,8 @@ def pre_norm_backward(dn: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, e
     dx = torch.empty_like(x)
     dw = torch.empty(H, dtype=torch.float32, device=dev)
     ws, nbytes = _norm_ws(ws, H, dev)
-    _call(dev, "qmoe_pre_norm_backward", _addr(dn), _addr(x), dt, _addr(weight), eps, _addr(dres), T,
-          H, dx.data_ptr(), dw.data_ptr(), _addr(ws), nbytes)
+    _call(dev, "qmoe_pre_norm_backward", _addr(dn), _addr(x), dt, _addr(weight), eps,
+          _addr(dres), T, H, dx.data_ptr(), dw.data_ptr(), _addr(ws), nbytes)
     return dx, dw
 
 
@@ -847,6 +846,6 @@ def post_norm_backward(dout: torch.Tensor, y: torch.Tensor, weight: torch.Tensor
          "dgate": None if gate is None else torch.empty_like(gate)}
     ws, nbytes = _norm_ws(ws, H, dev)
     _call(dev, "qmoe_post_norm_backward", _addr(dout), _addr(y), dt, _addr(weight), gp, kind, alpha,
-          eps, T, H, r["dy"].data_ptr(), r["dres"].data_ptr(), r["dw"].data_ptr(), _addr(r["dgate"]), _addr(ws),
-          nbytes)
+          eps, T, H, r["dy"].data_ptr(), r["dres"].data_ptr(), r["dw"].data_ptr(),
+          _addr(r["dgate"]), _addr(ws), nbytes)
     return r

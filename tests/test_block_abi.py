@@ -71,7 +71,8 @@ def test_fp8_grouped_matmul_refusals():
     for bad in (dict(pair_rows=2), dict(T=-1), dict(k=0), dict(k=9), dict(E=0), dict(block_m=48),
                 dict(N=0), dict(K=64), dict(K=0), dict(out_dtype=5), dict(T=1 << 30), dict(a=None),
                 dict(a_scale=None), dict(b=None), dict(b_scale=None), dict(srt=None),
-                dict(te=None), dict(off=None), dict(npad=None), dict(out=None), dict(a=ODD), dict(b=ODD)):
+                dict(te=None), dict(off=None), dict(npad=None), dict(out=None),
+                dict(a=ODD), dict(b=ODD)):
         assert c(**bad) == INV, bad
     assert c(E=2000) == UNS
     assert c(T=0, a=None) == OK
@@ -83,7 +84,8 @@ def test_balance_refusals():
     assert n >= 256 and n % 256 == 0 and ws(-1, 8) == 0 and ws(4, 0) == 0
     c = _caller("qmoe_balance", logits=P, ids=P, mask=None, T=6400, E=8, k=2, coef=0.1, loss=P,
                 counts=P, probs=P, tokens=P, ws=P, ws_bytes=n, stream=None)
-    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(E=64, k=17), dict(T=(1 << 29) + 1), dict(coef=NAN),
+    for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(E=64, k=17),
+                dict(T=(1 << 29) + 1), dict(coef=NAN),
                 dict(coef=INF), dict(logits=None), dict(ids=None), dict(loss=None),
                 dict(counts=None), dict(probs=None), dict(tokens=None), dict(ws=None),
                 dict(ws_bytes=n - 1), dict(ws=ODD)):
@@ -92,7 +94,8 @@ def test_balance_refusals():
     b = _caller("qmoe_balance_backward", logits=P, mask=None, counts=P, tokens=P, dloss=P, T=64,
                 E=8, k=2, coef=0.1, dlogits=P, stream=None)
     for bad in (dict(T=-1), dict(E=0), dict(k=0), dict(k=9), dict(T=(1 << 29) + 1), dict(coef=INF),
-                dict(logits=None), dict(counts=None), dict(tokens=None), dict(dloss=None), dict(dlogits=None)):
+                dict(logits=None), dict(counts=None), dict(tokens=None),
+                dict(dloss=None), dict(dlogits=None)):
         assert b(**bad) == INV, bad
     assert b(E=1025) == UNS
     assert b(T=0, logits=None) == OK

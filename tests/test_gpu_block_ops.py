@@ -180,7 +180,8 @@ MATMUL = [(1, 1, 128), (1, 2048, 2048), (2, 130, 256), (5, 63, 384), (15, 16, 12
           (17, 513, 640), (31, 33, 128), (33, 255, 256), (48, 1000, 384), (64, 256, 1024),
           (65, 129, 2304), (100, 384, 4096), (128, 128, 128), (129, 257, 384), (200, 200, 2048),
           (256, 256, 256), (300, 500, 640), (511, 777, 512), (640, 1024, 256), (1000, 129, 4224),
-          (2048, 300, 128), (2000, 2100, 384), (4100, 512, 256), (3700, 3650, 384), (3, 8192, 128), (8, 16, 8192)]
+          (2048, 300, 128), (2000, 2100, 384), (4100, 512, 256), (3700, 3650, 384),
+          (3, 8192, 128), (8, 16, 8192)]
 
 
 @pytest.mark.parametrize("b_block", [True, False])
@@ -299,7 +300,8 @@ def _grouped_check(out, ids, a, sa, b, sb, k, pair_rows, K):
 
 
 @pytest.mark.parametrize("bm", [16, 32, 64, 128])
-@pytest.mark.parametrize("T,E,k,N,K", [(1, 8, 2, 128, 128), (1, 1, 1, 5, 128), (4, 128, 8, 192, 256),
+@pytest.mark.parametrize("T,E,k,N,K", [(1, 8, 2, 128, 128), (1, 1, 1, 5, 128),
+                                       (4, 128, 8, 192, 256),
                                        (33, 16, 4, 257, 384), (100, 4, 2, 640, 256),
                                        (700, 8, 3, 130, 512), (2000, 3, 1, 513, 128)])
 def test_grouped_matmul(T, E, k, N, K, bm):
@@ -372,7 +374,7 @@ def test_grouped_matmul_over_many_experts_skewed(bm):
 @pytest.mark.parametrize("T,E,k,N,K", [(1200, 4, 2, 1100, 256), (3000, 8, 2, 2100, 128),
                                        (900, 64, 4, 1030, 128), (500, 60, 8, 1500, 256)])
 def test_grouped_matmul_large_tiles(T, E, k, N, K):
-    ids, al, b, sb = _grouped_case(T, E, k, N, K, ops.fp8_block_m(T, k, E), seed=T)
+    ids, al, b, sb = _grouped_case(T, E, k, N, K, ops.FP8_BLOCK_M, seed=T)
     q = ops.fp8_quant(_rand(T, K, seed=3))
     for dt in (BF, F32):
         out = torch.full((T * k, N), float("nan"), dtype=dt, device="cuda")
@@ -493,7 +495,8 @@ def test_balance_in_place_and_empty():
     one = torch.ones(1, device="cuda")
     dz = ops.balance_loss_backward(z, f["counts"], f["tokens"], 2, one)
     buf = z.clone()
-    assert torch.equal(ops.balance_loss_backward(buf, f["counts"], f["tokens"], 2, one, out=buf), dz)
+    got = ops.balance_loss_backward(buf, f["counts"], f["tokens"], 2, one, out=buf)
+    assert got is buf and torch.equal(buf, dz)
     f = ops.balance_loss(z[:0], ids[:0])
     assert float(f["loss"]) == 0 and not f["counts"].any() and not f["probs"].any()
     assert int(f["tokens"]) == 0
