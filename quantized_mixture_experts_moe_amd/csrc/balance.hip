@@ -9,7 +9,10 @@
 // token's logits in registers, EPL per lane, as in the routing kernel.  The
 // sums run in a fixed order (per wave over its tokens, over a block's waves,
 // then over the blocks in fp64), the counts are integer atomics, whose order
-// does not matter: results are the same bits on every run.
+// does not matter: results are the same bits on every run.  What bounds the
+// calls is latency: 8192 x 512 takes 7.4 us for the partial sums (2.3 TB/s),
+// 6.1 to join them, 10.8 for the gradient (3.1 TB/s); 64 x 8 takes 4.5 and 3.4.
+// 16-byte loads (four experts per lane) made the first and last 0.4 us slower.
 #include "block_common.h"
 
 namespace qmoe {

@@ -16,9 +16,13 @@
 // instruction, which sums in fp32 (7e-9 off on the same data) at half the
 // rate.
 //
-// b feeds the matrix core's row operand and a its
-// column operand, so a lane's results share one row of a (one scale) and are
-// consecutive columns of out.
+// b feeds the matrix core's row operand and a its column operand, so a lane's
+// results share one row of a (one scale) and are consecutive columns of out.
+//
+// Measured: 4096 x 4096 x 4096 in bf16 63-73 us (1.9-2.2 PFLOP/s, by the power
+// that the values draw), fp32 outputs of 1500 x 2048 x 4224 39 us (0.67), 2048
+// tokens on 128 experts of 1536 x 2048 123 us (3.7 TB/s), 4 tokens 17-19 us (4.8
+// TB/s), one row of 2048 x 2048 3.5 us (1.2 TB/s).
 #include "block_common.h"
 #include "qmoe_internal.h"
 
@@ -239,6 +243,13 @@ hipError_t launch_rows(const Fp8MatmulArgs& g, hipStream_t s) {
 // chunks are stored in the order c ^ (row / 2 % 8), so that the 16 rows that
 // are read together lie in different banks (the permutation is applied to the
 // memory addresses: the copy writes LDS in lane order).
+//
+// Bound, per K block of the 256 x 256 tile (1.30 us): the matrix core works
+// 46% of the time; without the repeated reads of a's fragments it would be
+// 1.10, without the scaling 1.17, without both 0.92.  fp32 outputs (a K block of
+// 128 x 128: 0.98 us): without copies, widening or scaling each about 0.1 less,
+// without all three 0.71; the widening instruction issues at the full rate and
+// hides behind the matrix core, so no form of the codes in LDS would save it.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Buffer descriptor of `bytes` bytes at p (raw, no swizzle); reads behind the

@@ -43,7 +43,9 @@ __device__ inline uint32_t amax8(const float v[8]) {
 // Row form.  A block covers 16 rows and kspan K blocks: 16 lanes hold one
 // group of 128 (8 values each), so a pass of 256 threads quantizes one K
 // block of 16 rows and writes its 16 scales side by side.  The next K block is
-// loaded before this one is worked on.
+// loaded before this one is worked on.  K is split until 2048 blocks are there.
+// SiLU(gate) * up of 16384 x 768 in bf16: 13.3 us, 4.7 TB/s of the 5.1 that a
+// large copy reaches.
 template <bool F32, bool ACT>
 __global__ __launch_bounds__(256) void fp8_quant_rows_kernel(const void* __restrict__ x, int M,
                                                              int K, int KB, int kspan, bool vec,
@@ -76,8 +78,10 @@ __device__ inline uint32_t lanes8_max(uint32_t x) {
 // Column form, both forms, or 128 x 128 blocks.  A block of 512 threads holds
 // a 128 x 128 tile in registers (16 lanes per row, 4 rows per thread); the
 // columns pass through LDS 64 at a time (33 KiB: four blocks per CU, against
-// two with the whole tile there), where eight lanes take a column, 16 rows
-// each, so that they write 128 consecutive bytes.
+// two with the whole tile there, 22 us instead of 15.5), where eight lanes take
+// a column, 16 rows each, so that they write 128 consecutive bytes.  Both forms
+// of 4111 x 2048 in fp32: 15.5 us, 3.3 TB/s; the 528 blocks are on the chip at
+// once and read together, then write together.
 constexpr int kTileThreads = 512, kPitch = 65;
 template <bool F32, bool ACT, bool BLOCK>
 __global__ __launch_bounds__(kTileThreads) void fp8_quant_tile_kernel(
