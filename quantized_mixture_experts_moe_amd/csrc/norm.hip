@@ -149,11 +149,28 @@ __device__ inline float rms_inv(float sumsq, int H, float eps) {
   return 1.0f / sqrtf(sumsq / (float)H + eps);
 }
 
-// The forward norms' r: the sum of squares in fp64 and the mean rounded once,
-// so that r, and with it every rounding decision behind it (the stored out,
-// the codes), does not depend on how a row is spread over threads.
+// Rows of the gradients whose sum of squares is near the end of fp32's range are
+// taken times kShrink instead: h is the same, and the norm's gradient is kShrink
+// times that of the smaller row.
+constexpr float kLarge = 0x1p120f, kShrink = 0x1p-72f;
+// (The row's gradient d is hidden from the compiler, so that it keeps no product
+// of it in registers for this rare second pass.)
 template <class S>
-__device__ inline float row_rms_inv(const float x[S::NV][8], int H, float eps, double* red) {
+__device__ inline void shrink(float v[S::NV][8], float d[S::NV][8]) {
+#pragma unroll
+  for (int i = 0; i < S::NV; i++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      v[i][j] *= kShrink;
+      asm("" : "+v"(d[i][j]));
+    }
+}
+
+// The forward norms' r in fp64, from a sum of squares in fp64: it does not
+// depend on how a row is spread over threads, and rows whose squares are beyond
+// fp32 keep it.
+template <class S>
+__device__ inline double row_rms_inv(const float x[S::NV][8], int H, float eps, double* red) {
   double s = 0.0;
 #pragma unroll
   for (int v = 0; v < S::NV; v++)
@@ -169,7 +186,7 @@ __device__ inline float row_rms_inv(const float x[S::NV][8], int H, float eps, d
 #pragma unroll
     for (int i = 1; i < S::WAVES; i++) s += red[i];
   }
-  return rsqrtf((float)(s / H) + eps);
+  return rsqrt(s / H + (double)eps);
 }
 
 // Writes a row of normed values in the form asked for.  `grp` (LDS, 128
@@ -280,7 +297,7 @@ __global__ __launch_bounds__(S::BLOCK) void pre_norm_kernel(const void* __restri
   float v[S::NV][8], wt[S::NV][8];
   load_row<S, F32>(x, live ? row : (size_t)T - 1, H, tr, v);
   load_row<S, true>(w, 0, H, tr, wt);
-  const float r = row_rms_inv<S>(v, H, eps, lds.red64);
+  const float r = (float)row_rms_inv<S>(v, H, eps, lds.red64);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
@@ -322,7 +339,7 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_kernel(
   load_row<S, F32>(x, rd, H, tr, res);
   load_gate<S, F32, G>(gate, rd, H, tr, g);
   load_row<S, true>(w, 0, H, tr, t);
-  const float r = row_rms_inv<S>(v, H, eps, lds.red64);
+  const float r = (float)row_rms_inv<S>(v, H, eps, lds.red64);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
@@ -337,7 +354,7 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_kernel(
   if (live) store_row<S, F32>(out, row, H, tr, v);
   if (w2 == nullptr) return;
   load_row<S, true>(w2, 0, H, tr, t);
-  const float r2 = row_rms_inv<S>(v, H, eps, lds.red64);
+  const float r2 = (float)row_rms_inv<S>(v, H, eps, lds.red64);
 #pragma unroll
   for (int i = 0; i < S::NV; i++)
 #pragma unroll
@@ -397,14 +414,23 @@ __global__ __launch_bounds__(S::BLOCK) void pre_norm_backward_kernel(
     float v[S::NV][8], d[S::NV][8];
     load_row<S, F32>(x, rd, H, tr, v);
     load_row<S, F32>(dn, rd, H, tr, d);
-    float ss = sum_sq<S>(v), sd = 0.f;
+    float ss, sd, scale = 1.f;
+    auto sums = [&]() {
+      ss = sum_sq<S>(v), sd = 0.f;
 #pragma unroll
-    for (int i = 0; i < S::NV; i++)
+      for (int i = 0; i < S::NV; i++)
 #pragma unroll
-      for (int j = 0; j < 8; j++) sd = __builtin_fmaf(d[i][j] * wt[i][j], v[i][j], sd);
-    row_sum2<S>(ss, sd, lds.red);
-    const float r = rms_inv(ss, H, eps);
-    const float c = sd * r * r / (float)H;  // mean(dh * h) * r
+        for (int j = 0; j < 8; j++) sd = __builtin_fmaf(d[i][j] * wt[i][j], v[i][j], sd);
+      row_sum2<S>(ss, sd, lds.red);
+    };
+    sums();
+    if (ss > kLarge) {  // the same for the whole row
+      scale = kShrink;
+      shrink<S>(v, d);
+      sums();
+    }
+    const float r = rms_inv(ss, H, eps * scale * scale), rs = r * scale;
+    const float c = sd * r * rs / (float)H;  // mean(dh * h) * r
     if (!live) continue;  // no barrier below this point of the loop
 #pragma unroll
     for (int i = 0; i < S::NV; i++)
@@ -412,7 +438,7 @@ __global__ __launch_bounds__(S::BLOCK) void pre_norm_backward_kernel(
       for (int j = 0; j < 8; j++) {
         const float h = v[i][j] * r;
         dw[i][j] = __builtin_fmaf(d[i][j], h, dw[i][j]);
-        v[i][j] = r * (d[i][j] * wt[i][j]) - h * c;
+        v[i][j] = rs * (d[i][j] * wt[i][j]) - h * c;
       }
     if (dres != nullptr) {
       load_row<S, F32>(dres, row, H, tr, d);
@@ -450,20 +476,29 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_backward_kernel(
     load_row<S, F32>(dout, rd, H, tr, d);
     load_gate<S, F32, G>(gate, rd, H, tr, g);
     // ss = sum v^2, sd = sum dh * v, st = sum dout * w * v (the token gate's).
-    float ss = sum_sq<S>(v), sd = 0.f, st = 0.f;
+    float ss, sd, st, scale = 1.f;
+    auto sums = [&]() {
+      ss = sum_sq<S>(v), sd = 0.f, st = 0.f;
 #pragma unroll
-    for (int i = 0; i < S::NV; i++)
+      for (int i = 0; i < S::NV; i++)
 #pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const float p = d[i][j] * wt[i][j] * v[i][j];
-        st += p;
-        sd = __builtin_fmaf(p, g[i][j], sd);
-      }
-    row_sum2<S>(ss, sd, lds.red);
+        for (int j = 0; j < 8; j++) {
+          const float p = d[i][j] * wt[i][j] * v[i][j];
+          st += p;
+          sd = __builtin_fmaf(p, g[i][j], sd);
+        }
+      row_sum2<S>(ss, sd, lds.red);
+    };
+    sums();
+    if (ss > kLarge) {  // the same for the whole row
+      scale = kShrink;
+      shrink<S>(v, d);
+      sums();
+    }
     if constexpr (G == QMOE_GATE_TOKEN)
       if (dgate) st = row_sum<S>(st, lds.red);
-    const float r = rms_inv(ss, H, eps);
-    const float c = sd * r * r / (float)H;
+    const float r = rms_inv(ss, H, eps * scale * scale), rs = r * scale;
+    const float c = sd * r * rs / (float)H;
     if (!live) continue;  // no barrier below this point of the loop
     if (G == QMOE_GATE_TOKEN && dgate && tr == 0) reinterpret_cast<float*>(dgate)[row] = st * r;
     float o[S::NV][8];
@@ -473,7 +508,7 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_backward_kernel(
       for (int j = 0; j < 8; j++) {
         const float h = v[i][j] * r, du = d[i][j] * g[i][j];
         dw[i][j] = __builtin_fmaf(du, h, dw[i][j]);
-        o[i][j] = r * (du * wt[i][j]) - h * c;
+        o[i][j] = rs * (du * wt[i][j]) - h * c;
         v[i][j] = d[i][j] * h * wt[i][j];  // the gate's gradient
         d[i][j] *= alpha;
       }
