@@ -84,3 +84,48 @@ def test_rows_of_other_sizes_keep_their_gradients(H):
     rest = [0, 1, 2, 3, 4, 6, 7]
     assert torch.equal(ops.pre_norm_backward(d, x, w)[0][rest], dx[rest])
     assert torch.equal(ops.post_norm_backward(d, x, w)["dy"][rest], y[rest])
+
+
+# ---------------------------------------------------------------- the stored out
+
+def _bf16(v):
+    """v (float64) rounded to bf16 once (8 significant bits, ties to even)."""
+    step = torch.exp2(torch.frexp(v).exponent.double() - 8)
+    return torch.round(v / step) * step
+
+
+@pytest.mark.parametrize("T,H", [(3000, 333), (2000, 512), (1000, 1000), (1030, 2048), (300, 4096),
+                                 (130, 8192), (67, 16384), (150, 8191)])
+@pytest.mark.parametrize("cancel", [False, True])
+def test_bf16_out_is_rounded_once(T, H, cancel):
+    """out is the definition's value rounded to bf16 once, so what the next norm
+    makes of it in fp32 (n, scales) is off by fp32 steps, not by bf16 ones.
+    cancel: x takes away most of the gated norm."""
+    y, w, w2 = _rand(T, H, seed=H), 1 + 0.3 * _rand(H, seed=2), 1 + 0.3 * _rand(H, seed=3)
+    y = (y * torch.exp(_rand(T, 1, seed=5))).to(BF)
+    gates = [None, 0.5 + _rand(H, seed=11), torch.sigmoid(_rand(T, 1, seed=12)),
+             torch.sigmoid(_rand(T, H, seed=13)).to(BF)]
+    forms = ["f32", "e4m3_128", "e4m3", "int8"]
+    for i, gate in enumerate(gates):
+        alpha = (1.0, 0.3, -0.5, 0.7)[i]
+        al32 = float(torch.tensor(alpha))
+        u = R.norm(y.double(), w.double(), EPS32) * (1.0 if gate is None else gate.double())
+        x = (-u / alpha if cancel else _rand(T, H, seed=9) * 2).to(BF)
+        want = _bf16(al32 * x.double() + u)
+        out, _, _ = ops.post_norm(y, w, x, gate=gate, alpha=alpha, eps=EPS)
+        bad = out.double() != want
+        assert not bad.any(), f"gate {i}: {int(bad.sum())} of {bad.numel()}"
+        o2, n, scale = ops.post_norm(y, w, x, gate=gate, alpha=alpha, eps=EPS, next_weight=w2,
+                                     next_out=forms[i])
+        assert torch.equal(o2, out)
+        ref = R.norm(want, w2.double(), EPS32)
+        # r, v r and the product with w: half a step each, and one for their products
+        rel = 4 * R.U32
+        if forms[i] == "f32":
+            assert ((n.double() - ref).abs() <= ref.abs() * rel + R.TINY).all()
+        else:
+            g = R.pad_to(ref, R.up128(H), 1).view(T, -1, 128) if forms[i] == "e4m3_128" \
+                else ref.view(T, 1, H)
+            s = R.group_scale(g.abs().amax(2), 127.0 if forms[i] == "int8" else 448.0)
+            got = scale.t() if forms[i] == "e4m3_128" else scale.view(T, 1)
+            assert ((got.double() - s).abs() <= s * (rel + R.U32)).all()
