@@ -200,15 +200,26 @@ struct Quant {
 // improved by one Newton step.  (The library's exponential and an IEEE
 // division cost twice the instructions, and the quantizer's time is these.)
 __device__ inline float silu_mul(float g, float u) {
-  const float hi = g * -1.44269502162933349609375f;
-  const float lo = __builtin_fmaf(g, -1.44269502162933349609375f, -hi) - g * 1.925963033500e-8f;
+  // Outside [-1000, 128] SiLU(g) is 0 or g; the product below stays finite.
+  const float c = __builtin_amdgcn_fmed3f(g, -1000.0f, 128.0f);
+  const float hi = c * -1.44269502162933349609375f;
+  const float lo = __builtin_fmaf(c, -1.44269502162933349609375f, -hi) - c * 1.925963033500e-8f;
+  if (hi >= 100.0f) {
+    // 1 does not count beside the power, which is near the end of fp32's range
+    // or beyond: g 2^-hi u with the whole part of hi applied last, u made
+    // smaller before, so that no step but the last leaves the range.
+    if (!(g > -INFINITY)) return __uint_as_float(0x7fc00000u);  // -inf or NaN
+    const float n = rintf(hi);
+    float e = __builtin_amdgcn_exp2f(n - hi);
+    e = __builtin_fmaf(e, lo * -0.693147180559945f, e);
+    return ldexpf(c * e * (u * 0x1p-32f), 32 - (int)n);
+  }
   float e = __builtin_amdgcn_exp2f(hi);
   e = __builtin_fmaf(e, lo * 0.693147180559945f, e);
   const float d = 1.0f + e;
   float r = __builtin_amdgcn_rcpf(d);
   r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-  // A power that overflows: SiLU is -0, and the step above has no meaning.
-  return (hi >= 126.0f ? g * 0.0f : g * r) * u;
+  return g * r * u;
 }
 
 }  // namespace bk
