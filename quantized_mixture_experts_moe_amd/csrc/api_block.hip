@@ -23,7 +23,7 @@ struct BalanceWs {
 };
 BalanceWs balance_ws_layout(int T, int E) {
   BalanceWs w{};
-  if (balance_small(T, E)) return w;
+  if (balance_small(T)) return w;
   const size_t nb = balance_blocks(T);
   w.csum = align_up(nb * E * 4, 256);
   w.nsum = align_up(w.csum + nb * E * 4, 256);

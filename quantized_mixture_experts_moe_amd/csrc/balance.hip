@@ -264,9 +264,14 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(
 
 }  // namespace
 
-// One block reads about 50 GB/s: up to 128 KiB of logits it is done before a
-// second launch could start.
-bool balance_small(int T, int E) { return (long long)T * E <= 32768; }
+// A wave takes a token at a time whatever E is, so what the one block costs goes
+// by its tokens: up to six per wave it is done before the second launch of the
+// other form would be.  One block / two launches, us on the GPU, by tokens:
+//   experts        16           64           96          112          4096
+//   8           3.1 / 5.7    4.8 / 5.8    6.0 / 6.0    6.4 / 5.9    140 / 7.0
+//   256         3.2 / 7.4    5.2 / 7.7    6.8 / 7.8    7.3 / 7.7
+//   1024        4.6 / 11.3   8.8 / 11.5  11.7 / 11.6  13.1 / 11.6
+bool balance_small(int T) { return T <= 6 * kSmallWaves; }
 int balance_blocks(int T) {
   const int need = (T + kWaves - 1) / kWaves;
   return need < 1 ? 1 : need > 256 ? 256 : need;
@@ -282,7 +287,7 @@ int balance_blocks(int T) {
 hipError_t launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                           int E, int k, float coef, float* loss, int32_t* counts, float* probs,
                           int32_t* tokens, const BalanceParts& w, hipStream_t s) {
-  if (balance_small(T, E)) {
+  if (balance_small(T)) {
 #define QMOE_CALL(EPL)                                                                           \
   hipLaunchKernelGGL(balance_small_kernel<EPL>, dim3(1), dim3(64 * kSmallWaves), 0, s, logits,    \
                      ids, mask, T, E, k, coef, loss, counts, probs, tokens);

@@ -58,7 +58,7 @@ struct BalanceParts {
   double* terms;
   int32_t* arrived;
 };
-bool balance_small(int T, int E);
+bool balance_small(int T);
 int balance_blocks(int T);
 hipError_t launch_balance(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                           int E, int k, float coef, float* loss, int32_t* counts, float* probs,
