@@ -713,7 +713,7 @@ hipError_t launch_tile(Fp8MatmulArgs g, hipStream_t s, int splits = 1) {
   const long long ntm = GROUPED ? g.M / C::BM + (g.E < g.P ? g.E : g.P) : (g.M + C::BM - 1) / C::BM;
   const long long total = (long long)((g.N + C::BN - 1) / C::BN) * ntm;
   if (total > (1ll << 30)) return hipErrorInvalidValue;
-  g.split_kb = (g.KB + splits - 1) / splits;
+  g.split_kb = (g.KB + splits - 1) / splits;  // (a part of `splits` has one K block at least)
   hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, EXACT, OUT32>),
                      dim3((unsigned)((total + 7) / 8 * 8), splits), dim3(C::THREADS), 0, s, g);
   return hipGetLastError();
@@ -774,7 +774,8 @@ Plan plan(int M, int N, int K, bool big) {
   if (tiles(64, 64) <= 2 * cus) {
     int s = 8;
     while (s > 1 && (tiles(64, 64) * s > cus || KB / s < 6)) s /= 2;
-    return {kSmall, s};
+    const int per = (KB + s - 1) / s;
+    return {kSmall, (KB + per - 1) / per};  // no part without a K block
   }
   if (tiles(64, 128) <= 2 * cus) return {kHalf, 1};
   const long long mid = (tiles(128, 128) + 2 * cus - 1) / (2 * cus);
