@@ -439,21 +439,24 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void fp8_matmul_tile_kernel(Fp8M
     sv = 4u * (unsigned)(n0 + (wave - C::AS) * 64 + lane);
   }
   // Copy c of the wave's COPIES of K block kb, to stage st.  (K blocks behind
-  // the last one are copies of nothing, from empty buffers.)
+  // the last one are copies of nothing, from empty buffers.)  The row is in the
+  // lane's offset, which alone is behind the buffer for a row behind its last
+  // one; the wave's is the place in the row.
   auto load = [&](uint8_t* st, int kb, int c) {
     const bool any = kb < kb1;
+    const unsigned at = any ? kb * 128 : 0;
     if (c < C::AC) {
       const int t = wave * C::AC + c;
       const Rsrc ra = rsrc(abase, any ? abytes : 0);
       if constexpr (GROUPED)
-        copy16(ra, av[c], kb * 128, st + t * 1024);
+        copy16(ra, av[c], at, st + t * 1024);
       else
-        copy16(ra, (C::AC % 2 == 0 ? c : t) % 2 ? av[1] : av[0], t * 8 * g.K + kb * 128,
+        copy16(ra, ((C::AC % 2 == 0 ? c : t) % 2 ? av[1] : av[0]) + t * 8 * (unsigned)g.K, at,
                st + t * 1024);
     } else if (c < C::AC + C::BC) {
       const int i = c - C::AC, t = wave * C::BC + i;
       const Rsrc rb = rsrc(bbase, any ? bbytes : 0);
-      copy16(rb, (C::BC % 2 == 0 ? i : t) % 2 ? bv[1] : bv[0], t * 8 * g.K + kb * 128,
+      copy16(rb, ((C::BC % 2 == 0 ? i : t) % 2 ? bv[1] : bv[0]) + t * 8 * (unsigned)g.K, at,
              st + C::B_AT + t * 1024);
     } else {
       const Rsrc rs = rsrc(sbase + (any ? (size_t)kb * sstep : 0), any ? sbytes : 0);
