@@ -1,7 +1,9 @@
-"""The fp8 products where K is split over blocks, and how exact they are."""
+"""The fp8 products where K is split over blocks, how exact they are, and the
+gradients of a linear layer made of them."""
 import pytest
 import torch
 
+import _block_ref as R
 from quantized_mixture_experts_moe_amd import ops
 from test_gpu_block_ops import test_matmul as check_matmul
 
@@ -29,3 +31,100 @@ def test_no_part_of_k_is_empty():
         parts = max(1, need // (4 * 64 * 64))
         per = -(-kb // parts)
         assert (parts - 1) * per < kb, (kb, parts)
+
+
+def _rand(*shape, seed):
+    g = torch.Generator("cuda")
+    g.manual_seed(seed)
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _off(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+@pytest.mark.parametrize("b_block", [True, False])
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 2048), (24, 500, 512), (64, 192, 2048),
+                                   (130, 513, 1024), (640, 1100, 256), (1500, 2048, 384),
+                                   (64, 256, 6272)])
+def test_fp32_products_are_sums_in_fp32(M, N, K, b_block):
+    """fp32 outputs against the 64-bit product in the 2-norm.  The products of
+    codes are exact; a K block's 128 are added in fp32, whatever the order at
+    most 128 roundings of the running sum, each at most a whole place (2^-23 of
+    it, for sums that are cut off), then two scale roundings and an addition
+    per K block.  The running sum of values of either sign is as large as the
+    result in the mean square, or smaller, and the roundings are independent:
+    sqrt(128) and sqrt(K / 128) of them.  The fp8 instruction's sums are 1.4e-5
+    off, bf16 operands that were rounded would be 2e-3."""
+    a = ops.fp8_quant(_rand(M, K, seed=1))
+    b = ops.fp8_quant(_rand(N, K, seed=2), block=b_block)
+    got = ops.fp8_matmul(a["codes"], a["scale"], b["codes"], b["scale"], b_block=b_block,
+                         out_dtype=torch.float32)
+    ref = R.wide(a["codes"], a["scale"]) @ R.wide(b["codes"], b["scale"], b_block).t()
+    bound = 2.0 ** -23 * (128 ** 0.5 + (3 * K / 128) ** 0.5)
+    assert bound < 4e-6 and _off(got, ref) <= bound
+
+
+@pytest.mark.parametrize("T,E,k,N,K", [(1, 8, 2, 128, 512), (64, 16, 4, 384, 1024),
+                                       (700, 8, 3, 130, 512), (1200, 4, 2, 1100, 256)])
+def test_fp32_grouped_products_are_sums_in_fp32(T, E, k, N, K):
+    ids = _rand(T, E, seed=3).topk(k, 1).indices.to(torch.int32)
+    al = ops.align(ids.contiguous(), E, ops.FP8_BLOCK_M)
+    a = ops.fp8_quant(_rand(T, K, seed=4))
+    b = ops.fp8_quant(_rand(E, N, K, seed=5), block=True)
+    got = ops.fp8_grouped_matmul(a["codes"], a["scale"], b["codes"], b["scale"], al, k,
+                                 out_dtype=torch.float32)
+    ref = torch.zeros(T * k, N, dtype=torch.float64, device="cuda")
+    av = R.wide(a["codes"], a["scale"])
+    for e in range(E):
+        p = (ids.reshape(-1) == e).nonzero().reshape(-1)
+        if p.numel():
+            ref[p] = av[p // k] @ R.wide(b["codes"][e], b["scale"][e], True).t()
+    assert _off(got, ref) <= 2.0 ** -23 * (128 ** 0.5 + (3 * K / 128) ** 0.5)
+
+
+# ---------------------------------------------------------------- a linear layer
+
+def _linear(T, N, K):
+    """x, w, dy and the layer's three products through the quantizer."""
+    x, w, dy = _rand(T, K, seed=1), _rand(N, K, seed=2), _rand(T, N, seed=3)
+    qw = ops.fp8_quant(w, block=True, cols=True)
+    qx, qy = ops.fp8_quant(x, cols=True), ops.fp8_quant(dy, cols=True)
+    f32 = torch.float32
+    y = ops.fp8_matmul(qx["codes"], qx["scale"], qw["codes"], qw["scale"], out_dtype=f32)
+    dx = ops.fp8_matmul(qy["codes"], qy["scale"], qw["codes_t"], qw["scale_t"], out_dtype=f32)
+    dw = ops.fp8_matmul(qy["codes_t"], qy["scale_t"], qx["codes_t"], qx["scale_t"], b_block=False,
+                        out_dtype=f32)
+    return x.double(), w.double(), dy.double(), y, dx, dw
+
+
+# What quantizing both factors leaves of a product, in the 2-norm: a code is off
+# by half a step at most, 2^-4 of the value, so 2^-4 / sqrt(3) in the mean square
+# (values below the normal range of a group add nothing that counts), and the two
+# factors' errors are independent.
+QUANT = 2.0 ** -4 * (2.0 / 3.0) ** 0.5
+
+
+@pytest.mark.parametrize("T,N,K", [(300, 200, 256), (130, 384, 128), (513, 130, 512)])
+def test_linear_layer_gradients_follow_the_loss(T, N, K):
+    """The three products against those of the values that were quantized, in 64
+    bits: a gradient that is missing, of another size, of other sources or
+    transposed is 1 off or so.  And differences of the loss sum(dy * (x w^T))
+    along each gradient are its own size: half, double or none of it is not."""
+    x, w, dy, y, dx, dw = _linear(T, N, K)
+    for got, ref in ((y, x @ w.t()), (dx[:, :K], dy @ w), (dw, dy.t() @ x)):
+        assert _off(got, ref) <= QUANT
+
+    def loss(xx, ww):
+        return (dy * (xx @ ww.t())).sum()
+    h = 1e-3  # (the loss is linear in each: differences are exact)
+    for grad, diff in ((dx[:, :K].double(), lambda d: loss(x + h * d, w) - loss(x - h * d, w)),
+                       (dw.double(), lambda d: loss(x, w + h * d) - loss(x, w - h * d))):
+        along = float(diff(grad)) / (2 * h)
+        size = float((grad * grad).sum())
+        # <true, grad> = |grad|^2 - <error, grad>, and |error| <= QUANT |true|,
+        # |true| <= |grad| / (1 - QUANT)
+        for scale, fits in ((1.0, True), (0.0, False), (0.5, False), (2.0, False), (-1.0, False)):
+            ok = abs(along * scale - size * scale * scale) <= size * scale * scale * \
+                QUANT / (1 - QUANT) and size * scale * scale > 0
+            assert ok == fits, scale
