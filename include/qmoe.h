@@ -28,8 +28,9 @@
  *    qmoe_check_flags, which synchronises the stream.
  *  - Arguments are validated on the host before anything is launched; on an
  *    error nothing is enqueued and the status says why.  No C++ exception
- *    crosses this interface.  T = 0 is valid: qmoe_align still writes its
- *    (empty) outputs, the other calls enqueue nothing.
+ *    crosses this interface.  T = 0 is valid: qmoe_align, qmoe_balance
+ *    and the norms' gradients still write the outputs that have no rows, the
+ *    other calls enqueue nothing.
  *  - Layouts are row-major with K contiguous.  int4 and e2m1 values are
  *    packed two per byte, the even K index in the low nibble.
  */
@@ -378,7 +379,8 @@ qmoe_status qmoe_fp8_quant(const void* x, int32_t dtype, int32_t B, int32_t M, i
  *   [ceil(N/128), K/128] (b_block = 1: weights) or [K/128, N] (b_block = 0).
  * out [M, N] bf16 or fp32 (out_dtype).  K % 128 == 0; any M and N.
  * The products of a K block are summed by the matrix cores, scaled once in
- * fp32 and added to an fp32 sum, K blocks in order; where the work is split
+ * fp32 (by sa * sb, which is to lie in fp32's normal range) and added to an
+ * fp32 sum, K blocks in order; where the work is split
  * along K (rules on the sizes) the parts are added in order, so a call gives
  * the same bits every time.  bf16 outputs take the fp8 matrix instruction,
  * whose sum of a K block is about 1.4e-5 off (2-norm; far below the output's

@@ -7,8 +7,9 @@
 //
 // The counts carry no gradient (they are whole numbers).  One wave holds a
 // token's logits in registers, EPL per lane, as in the routing kernel.  The
-// sums run in a fixed order (per wave over its tokens, over a block's waves,
-// then over the blocks in fp64), the counts are integer atomics, whose order
+// sums run in a fixed order (per wave over its tokens and over a block's waves
+// in fp32, which for terms that are not negative is a half step of the sum per
+// addition at most, then over the blocks in fp64), the counts are integer atomics, whose order
 // does not matter: results are the same bits on every run.  What bounds the
 // calls is latency: 8192 x 512 takes 7.4 us for the partial sums (2.3 TB/s),
 // 6.1 to join them, 10.8 for the gradient (3.1 TB/s); 64 x 8 takes 4.5 and 3.4.

@@ -211,12 +211,19 @@ template <int MS, bool GROUPED, bool BBLOCK, bool F32>
 hipError_t launch_rows(const Fp8MatmulArgs& g, hipStream_t s) {
   const int mt = (g.M + 16 * MS - 1) / (16 * MS);
   if (mt > 65535) return hipErrorInvalidValue;
-  // Where 32-column blocks fill the chip twice, four waves of two sub-tiles
-  // hold the most bytes under way per CU (64 tokens x 128 experts x 8 picks of
-  // 1536 x 2048: 67 us against 94 us with eight waves); else the latency of one
-  // block counts and K is split further, one sub-tile per block (1 x 2048 x
-  // 2048: 3.7 against 4.9 us), two where many rows of a would be read again by
-  // every block (16 x 8192 x 4096: 8.9 against 10.2 us).
+  // KS waves share K, NS sub-tiles share a block's rows of a.  Many waves read
+  // one column's K at once, which is what counts for a few blocks; few waves with
+  // two sub-tiles hold the most bytes under way where blocks fill the chip twice;
+  // two sub-tiles also halve how often a is read.  In us (K, rows x columns; the
+  // grouped ones: tokens of 8 picks on 128 experts):
+  //   KS x NS             4x2   16x2  16x1  8x1   4x1
+  //   2048, 64 t. x 1536   68    82   110    96    78   4x2: chip full
+  //   1024, 16 x 16384    5.6   5.7   7.6   6.3   6.4
+  //   4096, 16 x 8192    11.1   9.3  10.6  10.7  10.5   16x2: many columns, rows
+  //   4096, 32 x 4096    11.2  10.1   8.2   8.7   9.3   16x1: long K
+  //   8192, 1 x 1024     11.0  10.5   6.9   6.9   8.1
+  //   2048, 16 x 2048     5.7   5.3   4.3   4.3   4.7   8x1: half as long
+  //   512, 1 x 2048       2.6   2.8   2.5   2.4   2.3   4x1: four K blocks
   const long long blocks2 = (long long)mt * ((g.N + 31) / 32);
   const int cus = device_cu_count();
 #define QMOE_CALL(KS, NS, RING)                                                                \
@@ -244,12 +251,17 @@ hipError_t launch_rows(const Fp8MatmulArgs& g, hipStream_t s) {
 // are read together lie in different banks (the permutation is applied to the
 // memory addresses: the copy writes LDS in lane order).
 //
-// Bound, per K block of the 256 x 256 tile (1.30 us): the matrix core works
-// 46% of the time; without the repeated reads of a's fragments it would be
-// 1.10, without the scaling 1.17, without both 0.92.  fp32 outputs (a K block of
-// 128 x 128: 0.98 us): without copies, widening or scaling each about 0.1 less,
-// without all three 0.71; the widening instruction issues at the full rate and
-// hides behind the matrix core, so no form of the codes in LDS would save it.
+// Bound: a K block of the 256 x 256 tile takes 1.74 us on random codes (4096 x
+// 4096 by K), 2048 of its clocks in the matrix core, at 2.17 GHz 54%; with
+// prologue, stores and the launch (10 us in all) the 4096^3 product keeps it
+// busy 45% of its time.  On zeros, which draw less power, the K block takes
+// 1.30 us: 1.10 without the repeated reads of a's fragments, 1.17 without the
+// scaling, 0.92 without both.  fp32 outputs: one 64 x 128 tile on a CU takes 0.69
+// us per K block, two take 1.00, the matrix core busy 30% and 42% of that.  On
+// the 128 x 128 tile (0.98 us) copies, widening and scaling are about 0.1 each,
+// and without all three it takes 0.71; the widening instruction issues at the
+// full rate and hides behind the matrix core, so no form of the codes in LDS
+// would save it.
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Buffer descriptor of `bytes` bytes at p (raw, no swizzle); reads behind the
@@ -743,7 +755,7 @@ hipError_t launch_split(Fp8MatmulArgs g, int splits, hipStream_t s) {
 }
 
 // The tiles, from the sharpest reuse of what a CU copies (64 KiB of operands
-// feed 32 x 2 matrix instructions per SIMD in Big, 16 KiB 2 in Small) to the
+// feed 32 matrix instructions per SIMD in Big, 16 KiB 2 in Small) to the
 // most blocks and the shortest latency.
 typedef Tile<256, 256, 2, 4, 2> Big;
 typedef Tile<128, 256, 2, 4, 3> Wide;
@@ -820,7 +832,12 @@ hipError_t dense(const Fp8MatmulArgs& g, hipStream_t s) {
 //   512 (32)                  90    84    86     92   102
 //   1024 (64)                131   108    96    101   109
 //   2048 (128)                            130   142   124
-// and a smaller one where that leaves CUs without a block.
+// and a smaller one where that leaves CUs without a block.  Low's two stages let
+// more blocks share a CU, LowFew's three serve a block that has one to itself
+// (us, Low / LowFew: 256 tokens of 8 on 128 experts of 2048 x 768 36.7 / 40.7;
+// 128 of 2 on 8 of 1536 x 2048 12.6 / 9.2).  The rules go by the mean, which is
+// known on the host: a router that sends most rows to few experts gets the tiles
+// of an even one.
 template <bool EXACT>
 hipError_t grouped(const Fp8MatmulArgs& g, hipStream_t s) {
   const double mean = (double)g.P / g.E;

@@ -398,7 +398,6 @@ template <class S>
 __device__ inline void write_partial(float* part, int H, int tr, float a[S::NV][8], float* buf) {
   if constexpr (S::RPB > 1) {
     const int slot = threadIdx.x / S::TPR;
-    constexpr int PITCH = S::TPR * S::NV * 8;
     __syncthreads();
 #pragma unroll
     for (int s = S::RPB - 1; s >= 1; s--) {
@@ -417,7 +416,6 @@ __device__ inline void write_partial(float* part, int H, int tr, float a[S::NV][
       }
       __syncthreads();
     }
-    (void)PITCH;
     if (slot != 0) return;
   }
   store_row<S, true>(part, blockIdx.x, H, tr, a);

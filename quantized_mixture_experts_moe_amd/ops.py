@@ -467,7 +467,9 @@ def decode_forward(scheme: str, logits: torch.Tensor, x: torch.Tensor,
 # ---------------------------------------------------------------- around the experts
 # Block-128 fp8 quantizer and products, balance loss, norms.  These check
 # shapes, types and devices here (ValueError), since the C ABI sees pointers
-# only, and run on the current stream of the tensors' device.
+# only, and run on the current stream of the tensors' device.  None of them
+# records itself for autograd, whatever its arguments require: gradients are calls
+# of their own.
 
 # These checks and look-ups stand in front of calls whose kernels take a few
 # microseconds, so messages are formed only when they are raised.
@@ -667,7 +669,9 @@ def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor
     -> SiLU*mul and quantization -> down product -> combine.  x [T, H] codes
     with x_scale [H/128, T] (fp8_quant or a norm's "e4m3_128" form); weights:
     w13 [E, 2I, H], w2 [E, H, I] codes and their 128 x 128 block scales
-    (fp8_quant(w, block=True)), H % 128 == 0, I % 128 == 0."""
+    (fp8_quant(w, block=True)), H % 128 == 0, I % 128 == 0.  Between the calls
+    values are rounded as they would be between calls of a user's own: gate/up
+    and the pairs' outputs to bf16, SiLU*mul to e4m3."""
     T, E = logits.shape
     _need(x.shape[0] == T, "x has %d rows, logits %d", x.shape[0], T)
     with torch.cuda.device(_one_device(logits, x)):
