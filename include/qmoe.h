@@ -471,8 +471,8 @@ qmoe_status qmoe_balance_backward(const float* logits, const uint8_t* mask, cons
  *   the residual stream, g the gate (QMOE_GATE_NONE: 1; COLUMN: fp32 [H];
  *   TOKEN: fp32 [T]; FULL: [T,H] in dtype).  With next_w it also writes n,
  *   the norm of the stored out with the weights next_w, in `form`: the same
- *   bits as qmoe_pre_norm of out.  A bf16 out is its exact value rounded
- *   once.  out may be x.                                                  */
+ *   bits as qmoe_pre_norm of out.  A bf16 out is its value as fp32 would
+ *   hold it (rounded once), rounded to bf16.  out may be x.               */
 typedef enum {
   QMOE_FORM_BF16 = 0,
   QMOE_FORM_F32 = 1,

@@ -196,20 +196,6 @@ __device__ inline double wide_here(float v) {
   return (double)v;
 }
 
-// v rounded to bf16 once.  (float)v alone would round twice: where it falls on
-// the border between two bf16 values and v does not, it steps back to v's side.
-__device__ inline float bf16_once(double v) {
-  uint32_t b = __float_as_uint((float)v);
-  if ((b & 0xffffu) == 0x8000u) {
-    const double size = fabs((double)__uint_as_float(b));
-    if (size > fabs(v))
-      b--;
-    else if (size < fabs(v))
-      b++;
-  }
-  return bf16_f32(f32_bf16(__uint_as_float(b)));
-}
-
 // Writes a row of normed values in the form asked for.  `grp` (LDS, 128
 // words) serves the column groups of rows that are not taken by vectors.
 template <class S>
@@ -348,9 +334,10 @@ __device__ inline void load_gate(const void* gate, size_t row, int H, int tr,
 // The next norm reads a bf16 out as stored, so a value that fp32 steps had left
 // on the other side of a bf16 border (3 of 10^5) would put a whole bf16 step
 // into an fp32 n or scale.  A sum that lies nearer to a border than the steps
-// may be off (five half steps of its terms, less than 2^-21 of them: about one
-// sum of 2000) is therefore formed again in fp64 and rounded once.  With that
-// check 4096 x 4096 with the next norm takes 32.3 us, without it 29.6.
+// may be off (five half steps of its terms, with the one that the exact sum is
+// off in fp32 less than 2^-21 of them: about one sum of 2000) is therefore formed
+// again in fp64 and rounded to fp32 once; that is what bf16 rounds.  With that
+// check 4096 x 4096 with the next norm takes 32.2 us, without it 29.6.
 template <class S, bool F32, int G>
 __global__ __launch_bounds__(S::BLOCK) void post_norm_kernel(
     const void* __restrict__ y, const void* x, const float* __restrict__ w,
@@ -376,9 +363,10 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_kernel(
       if constexpr (!F32) {  // as stored
         const float tie = __uint_as_float((__float_as_uint(o) & 0xffff0000u) | 0x8000u);
         const float err = __builtin_fmaf(0x1p-21f, fabsf(p) + fabsf(q), 0x1p-140f);
-        o = fabsf(o - tie) > err ? bf16_f32(f32_bf16(o))
-                                 : bf16_once(fma((double)alpha, (double)res[i][j],
-                                                 wide_here(v[i][j]) * t[i][j] * r * g[i][j]));
+        if (!(fabsf(o - tie) > err))
+          o = (float)fma((double)alpha, (double)res[i][j],
+                         wide_here(v[i][j]) * t[i][j] * r * g[i][j]);
+        o = bf16_f32(f32_bf16(o));
       }
       v[i][j] = o;
     }

@@ -89,7 +89,9 @@ def test_rows_of_other_sizes_keep_their_gradients(H):
 # ---------------------------------------------------------------- the stored out
 
 def _bf16(v):
-    """v (float64) rounded to bf16 once (8 significant bits, ties to even)."""
+    """v (float64) as fp32 holds it, rounded to bf16 (8 significant bits, ties to
+    even): what a conversion of the 64-bit value gives."""
+    v = v.float().double()
     step = torch.exp2(torch.frexp(v).exponent.double() - 8)
     return torch.round(v / step) * step
 
@@ -98,7 +100,7 @@ def _bf16(v):
                                  (130, 8192), (67, 16384), (150, 8191)])
 @pytest.mark.parametrize("cancel", [False, True])
 def test_bf16_out_is_rounded_once(T, H, cancel):
-    """out is the definition's value rounded to bf16 once, so what the next norm
+    """out is the definition's value, as fp32 holds it, in bf16, so what the next norm
     makes of it in fp32 (n, scales) is off by fp32 steps, not by bf16 ones.
     cancel: x takes away most of the gated norm."""
     y, w, w2 = _rand(T, H, seed=H), 1 + 0.3 * _rand(H, seed=2), 1 + 0.3 * _rand(H, seed=3)
