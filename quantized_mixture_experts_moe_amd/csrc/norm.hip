@@ -22,7 +22,7 @@
 // block in registers, then over the blocks in a second launch, in a fixed
 // order: the same bits on every run.
 //
-// In bf16: after with the next block's codes at 4096 x 4096 26 us (4.5 TB/s),
+// In bf16: after with the next block's codes at 4096 x 4096 28 us (4.2 TB/s),
 // its gradients with a gate per value at 4111 x 2048 25 + 4 us (4.0 TB/s in the
 // first launch); before at one row of 4096 3.0 us, which is latency.
 #include "block_common.h"
