@@ -28,9 +28,9 @@
  *    qmoe_check_flags, which synchronises the stream.
  *  - Arguments are validated on the host before anything is launched; on an
  *    error nothing is enqueued and the status says why.  No C++ exception
- *    crosses this interface.  T = 0 is valid: qmoe_align, qmoe_balance
- *    and the norms' gradients still write the outputs that have no rows, the
- *    other calls enqueue nothing.
+ *    crosses this interface.  T = 0 is valid: qmoe_align, qmoe_balance, the
+ *    norms' gradients and qmoe_grouped_wgrad still write the outputs that have
+ *    no rows, the other calls enqueue nothing.
  *  - Layouts are row-major with K contiguous.  int4 and e2m1 values are
  *    packed two per byte, the even K index in the low nibble.
  */
@@ -345,8 +345,9 @@ qmoe_status qmoe_decode(const qmoe_ffn_desc* d, const float* logits, const void*
 /* =====================================================================
  * Operators around the experts: matrix products in 8-bit floating point
  * with a scale for each block of 128 (dense, and for the experts of a
- * routed batch) with the quantizer that feeds them, the router's balance
- * loss, and the norms before and after a block.  The conventions at the top
+ * routed batch) with the quantizer that feeds them, the experts' products in
+ * bf16 with their gradients and the routed sum's, dense products with 4-bit
+ * weights, the router's balance loss, and the norms before and after a block.  The conventions at the top
  * of this file hold for them.  Arrays are contiguous.                    */
 
 /* ---------------------------------------------------------------------
@@ -417,6 +418,100 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
                                     const int32_t* expert_offsets, const int32_t* num_padded,
                                     int32_t T, int32_t k, int32_t E, int32_t block_m, int32_t N,
                                     int32_t K, void* out, int32_t out_dtype, void* stream);
+
+/* ---------------------------------------------------------------------
+ * The experts' products in bf16, the type they are trained in, and their
+ * gradients; sums in fp32.  sorted_pair_ids, tile_expert, expert_offsets and
+ * num_padded are qmoe_align's outputs for the same T, k, E and block_m (any
+ * block_m gives the same sums; 16 has the least padding).  N and K are multiples
+ * of 8, E <= 1024, every array 16-byte aligned; one matrix of b, and each array
+ * of rows, holds up to 3 GiB, rows up to 2^22 values (QMOE_ERR_UNSUPPORTED).
+ * Rows of pairs that qmoe_align dropped are left as they are in out and gu,
+ * and count nothing in dw.
+ *
+ * qmoe_grouped_matmul -- for every (token, slot) pair p with its expert e:
+ *     b_trans = 0: out[p] = a[row(p)] . b[e]^T, b [E, N, K] (a projection)
+ *     b_trans = 1: out[p] = a[row(p)] . b[e],   b [E, K, N] (the gradient of a
+ *                  projection's rows, a being that of its outputs)
+ *   a: pair_rows = 0: [T, K], row(p) = p / k; pair_rows = 1: [T*k, K], row(p) = p.
+ *   act: what is done with the sums before they are rounded to out's type (bf16
+ *   or fp32):
+ *     QMOE_ACT_NONE: nothing; out [T*k, N], gu NULL;
+ *     QMOE_ACT_SILU_MUL (b_trans 0): columns 0 .. N/2-1 are gates g, N/2 .. N-1
+ *       are u; out [T*k, N/2] = SiLU(g) * u (N / 2 a multiple of 8), and g | u
+ *       themselves, rounded to bf16, to gu [T*k, N] unless it is NULL;
+ *     QMOE_ACT_SILU_MUL_BACKWARD (b_trans 1): for a sum d, the gradient of
+ *       SiLU(g) * u, out [T*k, 2 N] = d u s (1 + g (1 - s)) | d g s with s =
+ *       1 / (1 + exp(-g)), g | u read from gu [T*k, 2 N].
+ *   A call gives the same bits every time.
+ *
+ * qmoe_grouped_wgrad -- dw[e] = sum over e's pairs p of dy[p]^T x[row(p)],
+ *   dw [E, N, K] bf16 or fp32, dy [T*k, N], x [T, K] or [T*k, K] as a above.
+ *   Experts without pairs get zeros.  accumulate = 1 (fp32): added to what dw
+ *   holds.  ws: qmoe_grouped_wgrad_workspace bytes (0: none needed, ws may be
+ *   NULL), 256-byte aligned, contents need no initialisation; calls that share
+ *   it must be ordered on one stream.                                       */
+typedef enum {
+  QMOE_ACT_NONE = 0,
+  QMOE_ACT_SILU_MUL = 1,
+  QMOE_ACT_SILU_MUL_BACKWARD = 2
+} qmoe_act;
+qmoe_status qmoe_grouped_matmul(const uint16_t* a, int32_t pair_rows, const uint16_t* b,
+                                int32_t b_trans, const int32_t* sorted_pair_ids,
+                                const int32_t* tile_expert, const int32_t* expert_offsets,
+                                const int32_t* num_padded, int32_t T, int32_t k, int32_t E,
+                                int32_t block_m, int32_t N, int32_t K, int32_t act, uint16_t* gu,
+                                void* out, int32_t out_dtype, void* stream);
+size_t qmoe_grouped_wgrad_workspace(int32_t T, int32_t k, int32_t E, int32_t N, int32_t K);
+qmoe_status qmoe_grouped_wgrad(const uint16_t* dy, const uint16_t* x, int32_t pair_rows,
+                               const int32_t* sorted_pair_ids, const int32_t* expert_offsets,
+                               int32_t T, int32_t k, int32_t E, int32_t block_m, int32_t N,
+                               int32_t K, void* dw, int32_t out_dtype, int32_t accumulate,
+                               void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------
+ * qmoe_combine_backward -- the gradients of qmoe_combine's sum and of
+ * qmoe_route's weights, for the gradient dout [T,H] of out:
+ *   dy[t*k+j]          = topk_w[t,j] * dout[t]          [T*k,H]
+ *   dtopk_w[t,j]       = <dout[t], y_pairs[t*k+j]>      fp32 [T,k]
+ *   dlogits[t,ids[t,j]] = w_j (dtopk_w_j - sum_i w_i dtopk_w_i), 0 for experts
+ *     that the token did not pick, + add[t,e] where add (fp32 [T,E], another
+ *     gradient of the logits, such as qmoe_balance_backward's; it may be
+ *     dlogits) is not NULL; fp32 [T,E], written whole.
+ * dout, y_pairs and dy are bf16 or fp32 (dtype); sums in fp32 in a fixed order.
+ * dtopk_w and dlogits may be NULL.  A pair whose id is outside [0,E) gets dy 0
+ * and dtopk_w 0, its y_pairs row is not read.  dy may be y_pairs.
+ * k <= 16, H % 8 == 0, E <= 1024; dout, y_pairs and dy 16-byte aligned.     */
+qmoe_status qmoe_combine_backward(const void* dout, const void* y_pairs, int32_t dtype,
+                                  const int32_t* topk_ids, const float* topk_w, int32_t T,
+                                  int32_t k, int32_t H, int32_t E, const float* add, void* dy,
+                                  float* dtopk_w, float* dlogits, void* stream);
+
+/* ---------------------------------------------------------------------
+ * qmoe_w4_matmul -- dense product with 4-bit weights:
+ *   out[m,n] = sum_g scale[n,g] * sum_{i<group} x[m, g*group+i] * q[n, g*group+i]
+ * x bf16 [M,K]; codes [N, K/2], two per byte, the even K index in the low
+ *   nibble.  format QMOE_W4_INT4: two's complement, scale fp16 [N, K/group],
+ *   group 32, 64 or 128 (32: an expert's matrix of QMOE_W4A16_G32 in the
+ *   canonical layout); QMOE_W4_MXFP4: e2m1, scale e8m0 [N, K/32], group 32.
+ * The weights are not rounded: a group's sum is formed over exact codes, in
+ *   fp32, and scaled once.
+ * act: QMOE_ACT_NONE, or QMOE_ACT_SILU_MUL: rows 0 .. N/2-1 of the weights are
+ *   gates and out [M, N/2] = SiLU(g) * u.  add: [.. as out, in its type], added
+ *   before the rounding, or NULL; it may be out.  out bf16 or fp32.
+ * x is to be finite and below 2^120: a row of x that holds an infinity or a NaN
+ *   gives a row of out that is not finite.
+ * ws: qmoe_w4_matmul_workspace(M, N, K) bytes (0: none needed, ws may be NULL),
+ *   256-byte aligned, contents need no initialisation; calls that share it must
+ *   be ordered on one stream.  K % group == 0; any M and N; x, codes and scale
+ *   16-byte aligned.  Limits: M, N <= 2^24, K <= 2^22 (QMOE_ERR_UNSUPPORTED).
+ * A call gives the same bits every time.                                  */
+typedef enum { QMOE_W4_INT4 = 0, QMOE_W4_MXFP4 = 1 } qmoe_w4_format;
+size_t qmoe_w4_matmul_workspace(int32_t M, int32_t N, int32_t K);
+qmoe_status qmoe_w4_matmul(const uint16_t* x, const uint8_t* codes, const void* scale,
+                           int32_t format, int32_t group, int32_t M, int32_t N, int32_t K,
+                           int32_t act, const void* add, void* out, int32_t out_dtype, void* ws,
+                           size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------
  * qmoe_balance -- the router's balance loss and per-expert counts.  With p

@@ -36,6 +36,18 @@ BalanceWs balance_ws_layout(int T, int E) {
 // A tile's rows of K bytes are addressed with 31-bit byte offsets.
 constexpr int kMaxK = 1 << 22;
 
+// Sizes of an expert-sorted list.
+bool valid_list(int32_t T, int32_t k, int32_t E, int32_t block_m) {
+  return T >= 0 && k >= 1 && E >= 1 && k <= E && (long long)T * k <= (1ll << 30) &&
+         (block_m == 16 || block_m == 32 || block_m == 64 || block_m == 128);
+}
+// A bf16 matrix that the grouped products do not address: they use 32-bit byte
+// offsets below 3 GiB (the kernels' offset of no row), and a tile's rows stay
+// below 2^31 bytes.
+bool too_large(uint64_t rows, uint64_t cols) {
+  return rows * cols * 2 > (3ull << 30) || cols > (1u << 22);
+}
+
 bool valid_form(int32_t form) { return form >= QMOE_FORM_BF16 && form <= QMOE_FORM_E4M3_B128; }
 bool form_scaled(int32_t form) { return form >= QMOE_FORM_INT8; }
 // `arrays`: those of H columns (nullptr for one that is not given).
@@ -158,6 +170,146 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
   g.E = E;
   g.pair_rows = pair_rows != 0;
   return hip_status(launch_fp8_grouped_matmul(g, (hipStream_t)stream));
+}
+
+qmoe_status qmoe_grouped_matmul(const uint16_t* a, int32_t pair_rows, const uint16_t* b,
+                                int32_t b_trans, const int32_t* sorted_pair_ids,
+                                const int32_t* tile_expert, const int32_t* expert_offsets,
+                                const int32_t* num_padded, int32_t T, int32_t k, int32_t E,
+                                int32_t block_m, int32_t N, int32_t K, int32_t act, uint16_t* gu,
+                                void* out, int32_t out_dtype, void* stream) {
+  if (!valid_list(T, k, E, block_m) || N < 8 || K < 8 || pair_rows < 0 || pair_rows > 1 ||
+      b_trans < 0 || b_trans > 1 || act < QMOE_ACT_NONE || act > QMOE_ACT_SILU_MUL_BACKWARD ||
+      !valid_dtype(out_dtype))
+    return QMOE_ERR_INVALID_ARG;
+  if ((act == QMOE_ACT_SILU_MUL && (b_trans || N % 2 != 0)) ||
+      (act == QMOE_ACT_SILU_MUL_BACKWARD && !b_trans) || (act == QMOE_ACT_NONE && gu != nullptr))
+    return QMOE_ERR_INVALID_ARG;
+  const int cols = act == QMOE_ACT_SILU_MUL ? N / 2 : N;
+  if (E > 1024 || K % 8 != 0 || cols % 8 != 0) return QMOE_ERR_UNSUPPORTED;
+  if (too_large((uint64_t)T * (pair_rows ? k : 1), K) || too_large(N, K) || too_large(K, N))
+    return QMOE_ERR_UNSUPPORTED;
+  if (T == 0) return QMOE_OK;
+  if (!a || !b || !sorted_pair_ids || !tile_expert || !expert_offsets || !num_padded || !out ||
+      (act == QMOE_ACT_SILU_MUL_BACKWARD && !gu))
+    return QMOE_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(gu, 16) || !aligned(out, 16))
+    return QMOE_ERR_INVALID_ARG;
+  GroupedArgs g{};
+  g.a = a;
+  g.b = b;
+  g.out = out;
+  g.gu = gu;
+  g.M = (int)qmoe_align_capacity(T, k, E, block_m);
+  g.Ma = pair_rows ? T * k : T;
+  g.N = N;
+  g.K = K;
+  g.trans = b_trans != 0;
+  g.out_f32 = out_dtype == QMOE_DT_F32;
+  g.act = act;
+  g.sorted = sorted_pair_ids;
+  g.tile_expert = tile_expert;
+  g.expert_offsets = expert_offsets;
+  g.num_padded = num_padded;
+  g.P = T * k;
+  g.k = k;
+  g.block_m = block_m;
+  g.E = E;
+  g.pair_rows = pair_rows != 0;
+  return hip_status(launch_grouped_matmul(g, (hipStream_t)stream));
+}
+
+size_t qmoe_grouped_wgrad_workspace(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+
+qmoe_status qmoe_grouped_wgrad(const uint16_t* dy, const uint16_t* x, int32_t pair_rows,
+                               const int32_t* sorted_pair_ids, const int32_t* expert_offsets,
+                               int32_t T, int32_t k, int32_t E, int32_t block_m, int32_t N,
+                               int32_t K, void* dw, int32_t out_dtype, int32_t accumulate,
+                               void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_list(T, k, E, block_m) || N < 8 || K < 8 || pair_rows < 0 || pair_rows > 1 ||
+      !valid_dtype(out_dtype) || accumulate < 0 || accumulate > 1 ||
+      (accumulate && out_dtype != QMOE_DT_F32))
+    return QMOE_ERR_INVALID_ARG;
+  if (E > 1024 || N % 8 != 0 || K % 8 != 0) return QMOE_ERR_UNSUPPORTED;
+  if (too_large((uint64_t)T * k, N) || too_large((uint64_t)T * (pair_rows ? k : 1), K))
+    return QMOE_ERR_UNSUPPORTED;
+  if ((T > 0 && (!dy || !x)) || !sorted_pair_ids || !expert_offsets || !dw)
+    return QMOE_ERR_INVALID_ARG;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dw, 16)) return QMOE_ERR_INVALID_ARG;
+  WgradArgs g{};
+  g.dy = dy;
+  g.x = x;
+  g.out = dw;
+  g.Mx = pair_rows ? T * k : T;
+  g.N = N;
+  g.K = K;
+  g.out_f32 = out_dtype == QMOE_DT_F32;
+  g.accumulate = accumulate != 0;
+  g.sorted = sorted_pair_ids;
+  g.expert_offsets = expert_offsets;
+  g.P = T * k;
+  g.k = k;
+  g.E = E;
+  g.pair_rows = pair_rows != 0;
+  return hip_status(launch_grouped_wgrad(g, (hipStream_t)stream));
+}
+
+qmoe_status qmoe_combine_backward(const void* dout, const void* y_pairs, int32_t dtype,
+                                  const int32_t* topk_ids, const float* topk_w, int32_t T,
+                                  int32_t k, int32_t H, int32_t E, const float* add, void* dy,
+                                  float* dtopk_w, float* dlogits, void* stream) {
+  if (!valid_dtype(dtype) || T < 0 || k < 1 || k > 16 || E < 1 || k > E || H < 8 || H % 8 != 0)
+    return QMOE_ERR_INVALID_ARG;
+  if ((long long)T * k > (1ll << 30)) return QMOE_ERR_INVALID_ARG;
+  if (add != nullptr && dlogits == nullptr) return QMOE_ERR_INVALID_ARG;
+  if (E > 1024) return QMOE_ERR_UNSUPPORTED;
+  if (T == 0) return QMOE_OK;
+  if (!dout || !y_pairs || !topk_ids || !topk_w || !dy) return QMOE_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(y_pairs, 16) || !aligned(dy, 16)) return QMOE_ERR_INVALID_ARG;
+  const CombineBwdArgs g{dout, y_pairs, dtype == QMOE_DT_F32, topk_ids, topk_w, add, T, k, H, E,
+                         dy,   dtopk_w, dlogits};
+  return hip_status(launch_combine_backward(g, (hipStream_t)stream));
+}
+
+size_t qmoe_w4_matmul_workspace(int32_t M, int32_t N, int32_t K) {
+  if (M < 0 || N < 1 || K < 32 || K % 32 != 0) return 0;
+  return align_up(w4_matmul_parts_bytes(M, N, K), 256);
+}
+
+qmoe_status qmoe_w4_matmul(const uint16_t* x, const uint8_t* codes, const void* scale,
+                           int32_t format, int32_t group, int32_t M, int32_t N, int32_t K,
+                           int32_t act, const void* add, void* out, int32_t out_dtype, void* ws,
+                           size_t ws_bytes, void* stream) {
+  if ((format != QMOE_W4_INT4 && format != QMOE_W4_MXFP4) || M < 0 || N < 1 || K < 32 ||
+      (act != QMOE_ACT_NONE && act != QMOE_ACT_SILU_MUL) || (act && N % 2 != 0) ||
+      !valid_dtype(out_dtype))
+    return QMOE_ERR_INVALID_ARG;
+  if ((group != 32 && group != 64 && group != 128) || (format == QMOE_W4_MXFP4 && group != 32) ||
+      K % group != 0)
+    return QMOE_ERR_INVALID_ARG;
+  if (M > (1 << 24) || N > (1 << 24) || K > kMaxK) return QMOE_ERR_UNSUPPORTED;
+  if (M == 0) return QMOE_OK;
+  if (!x || !codes || !scale || !out) return QMOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 16) ||
+      !aligned(add, elem(out_dtype)) || !aligned(out, elem(out_dtype)))
+    return QMOE_ERR_INVALID_ARG;
+  const size_t need = qmoe_w4_matmul_workspace(M, N, K);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned(ws, 256))) return QMOE_ERR_INVALID_ARG;
+  W4Args g{};
+  g.x = x;
+  g.codes = codes;
+  g.scale = scale;
+  g.mxfp4 = format == QMOE_W4_MXFP4;
+  g.group = group;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.act = act == QMOE_ACT_SILU_MUL;
+  g.out_f32 = out_dtype == QMOE_DT_F32;
+  g.add = add;
+  g.out = out;
+  g.parts = reinterpret_cast<float*>(ws);
+  return hip_status(launch_w4_matmul(g, (hipStream_t)stream));
 }
 
 size_t qmoe_balance_workspace(int32_t T, int32_t E) {

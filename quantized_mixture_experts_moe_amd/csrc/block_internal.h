@@ -48,6 +48,62 @@ size_t fp8_matmul_parts_bytes(int M, int N, int K);
 hipError_t launch_fp8_matmul(const Fp8MatmulArgs& g, hipStream_t s);
 hipError_t launch_fp8_grouped_matmul(const Fp8MatmulArgs& g, hipStream_t s);
 
+// bf16 products of the experts over qmoe_align's list.
+struct GroupedArgs {
+  const uint16_t* a;  // [Ma, K]
+  const uint16_t* b;  // [E, N, K]; trans [E, K, N]
+  void* out;          // [P, N]; SiLU * mul [P, N / 2]; its gradient [P, 2 N]
+  uint16_t* gu;       // SiLU * mul: [P, N] written, or nullptr; its gradient: [P, 2 N] read
+  int M, Ma, N, K;    // M: capacity of the list
+  bool trans, out_f32;
+  int act;            // qmoe_act
+  const int32_t* sorted;
+  const int32_t* tile_expert;
+  const int32_t* expert_offsets;
+  const int32_t* num_padded;
+  int P, k, block_m, E;
+  bool pair_rows;
+};
+struct WgradArgs {
+  const uint16_t* dy;  // [P, N]
+  const uint16_t* x;   // [Mx, K]
+  void* out;           // [E, N, K]
+  int Mx, N, K;
+  bool out_f32, accumulate;
+  const int32_t* sorted;
+  const int32_t* expert_offsets;
+  int P, k, E;
+  bool pair_rows;
+};
+hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t s);
+hipError_t launch_grouped_wgrad(const WgradArgs& g, hipStream_t s);
+
+struct CombineBwdArgs {
+  const void *dout, *y;
+  bool f32;
+  const int32_t* ids;
+  const float* w;
+  const float* add;
+  int T, k, H, E;
+  void* dy;
+  float *dw, *dlogits;
+};
+hipError_t launch_combine_backward(const CombineBwdArgs& g, hipStream_t s);
+
+struct W4Args {
+  const uint16_t* x;     // [M, K]
+  const uint8_t* codes;  // [N, K/2]
+  const void* scale;     // [N, K/group]
+  bool mxfp4;
+  int group, M, N, K;
+  bool act, out_f32;
+  const void* add;       // [M, columns of out] or nullptr
+  void* out;             // [M, N]; act [M, N / 2]
+  float* parts;          // sums of a K split
+};
+size_t w4_matmul_parts_bytes(int M, int N, int K);
+hipError_t launch_w4_matmul(const W4Args& g, hipStream_t s);
+
 // Workspace of the balance loss: per block (balance_blocks) the probability
 // sums and counts [E] and kept tokens; per 32 experts a term of the loss; the
 // blocks that have arrived.  A small batch needs none.

@@ -1,0 +1,133 @@
+// Gradient of the routed sum out[t] = sum_j w[t,j] y[t k + j] and of the
+// weights' softmax over the picked logits:
+//   dy[t k + j] = w[t,j] dout[t],   dw[t,j] = <dout[t], y[t k + j]>,
+//   dlogits[t, ids[t,j]] += w[t,j] (dw[t,j] - sum_i w[t,i] dw[t,i]).
+// Bound: y is read once and dy written once.  WPT waves take a token: a lane
+// holds eight columns of dout at a time and passes over the token's rows of y,
+// whose products it keeps for the rows of a group of kGroup.
+#include "block_common.h"
+#include "qmoe_internal.h"
+
+namespace qmoe {
+namespace {
+using namespace bk;
+constexpr int kGroup = 8, kMaxK = 16;
+
+template <int WPT, bool F32>
+__global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g) {
+  constexpr int TPB = 4 / WPT;  // tokens per block
+  __shared__ float sums[4][kMaxK];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int t = blockIdx.x * TPB + wave / WPT;
+  const bool on = t < g.T;
+  const int k = g.k, H = g.H;
+  const size_t p0 = (size_t)t * k;
+  const int c0 = ((wave % WPT) * 64 + lane) * 8, step = WPT * 512;
+  if (on) {
+    for (int j0 = 0; j0 < k; j0 += kGroup) {
+      float w[kGroup], dot[kGroup];
+      bool in[kGroup];  // the pair's id is an expert's
+#pragma unroll
+      for (int u = 0; u < kGroup; u++) {
+        dot[u] = 0.f;
+        in[u] = false;
+        w[u] = 0.f;
+        if (j0 + u < k) {
+          in[u] = (unsigned)g.ids[p0 + j0 + u] < (unsigned)g.E;
+          w[u] = g.w[p0 + j0 + u];
+        }
+      }
+      for (int c = c0; c < H; c += step) {
+        float d[8];
+        load8<F32>(g.dout, (size_t)t * H + c, d);
+        float y[kGroup][8];
+#pragma unroll
+        for (int u = 0; u < kGroup; u++)
+          if (in[u]) load8<F32>(g.y, (p0 + j0 + u) * H + c, y[u]);
+#pragma unroll
+        for (int u = 0; u < kGroup; u++) {
+          if (j0 + u >= k) break;
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[i] = in[u] ? w[u] * d[i] : 0.f;
+          store8<F32>(g.dy, (p0 + j0 + u) * H + c, v);
+          if (in[u]) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) dot[u] = __builtin_fmaf(d[i], y[u][i], dot[u]);
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kGroup; u++) {
+        if (j0 + u >= k) break;
+        const float s = wave_sum(dot[u]);
+        if (lane == 0) sums[wave][j0 + u] = s;
+      }
+    }
+  }
+  __syncthreads();
+  if (!on) return;
+  float dw[kMaxK], mean = 0.f;
+  const int first = wave / WPT * WPT;
+#pragma unroll
+  for (int j = 0; j < kMaxK; j++) {
+    dw[j] = 0.f;
+    if (j < k) {
+#pragma unroll
+      for (int v = 0; v < WPT; v++) dw[j] += sums[first + v][j];
+      mean = __builtin_fmaf(g.w[p0 + j], dw[j], mean);
+    }
+  }
+  const int at = (wave % WPT) * 64 + lane;
+  if (g.dw != nullptr) {
+#pragma unroll
+    for (int j = 0; j < kMaxK; j++)
+      if (j < k && at == j) g.dw[p0 + j] = dw[j];
+  }
+  if (g.dlogits != nullptr) {
+    float dz[kMaxK];
+    int id[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; j++) {
+      dz[j] = 0.f;
+      id[j] = -1;
+      if (j < k) {
+        dz[j] = g.w[p0 + j] * (dw[j] - mean);
+        id[j] = g.ids[p0 + j];
+      }
+    }
+    const size_t row = (size_t)t * g.E;
+    for (int e = at; e < g.E; e += WPT * 64) {
+      float v = g.add != nullptr ? g.add[row + e] : 0.f;
+#pragma unroll
+      for (int j = 0; j < kMaxK; j++)
+        if (j < k && id[j] == e) v += dz[j];
+      g.dlogits[row + e] = v;
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_combine_backward(const CombineBwdArgs& g, hipStream_t s) {
+  // A wave's pass covers 512 columns: one wave per token up to there.
+#define QMOE_CALL(WPT, F32)                                                                \
+  hipLaunchKernelGGL((combine_backward_kernel<WPT, F32>),                                  \
+                     dim3((unsigned)((g.T + 4 / WPT - 1) / (4 / WPT))), dim3(256), 0, s, g)
+  if (g.H <= 512) {
+    if (g.f32)
+      QMOE_CALL(1, true);
+    else
+      QMOE_CALL(1, false);
+  } else {
+    if (g.f32)
+      QMOE_CALL(4, true);
+    else
+      QMOE_CALL(4, false);
+  }
+#undef QMOE_CALL
+  return hipGetLastError();
+}
+
+}  // namespace qmoe

@@ -25,6 +25,7 @@
 // TB/s), one row of 2048 x 2048 3.5 us (1.2 TB/s).
 #include "block_common.h"
 #include "qmoe_internal.h"
+#include "tile_common.h"
 
 namespace qmoe {
 namespace {
@@ -33,7 +34,6 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-constexpr unsigned kNowhere = 0xC0000000u;  // an offset behind every buffer of gathered rows
 constexpr int kUnit = 127;  // e8m0 of 1: the instruction's own scales are not used
 
 __device__ inline i32x8 join(u32x4 lo, u32x4 hi) {
@@ -262,40 +262,6 @@ hipError_t launch_rows(const Fp8MatmulArgs& g, hipStream_t s) {
 // and without all three it takes 0.71; the widening instruction issues at the
 // full rate and hides behind the matrix core, so no form of the codes in LDS
 // would save it.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// Buffer descriptor of `bytes` bytes at p (raw, no swizzle); reads behind the
-// end give zeros.
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-__device__ inline Rsrc rsrc(const void* p, size_t bytes) {
-  const unsigned n = bytes < 0xfffffff0u ? (unsigned)bytes : 0xfffffff0u;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)n, 0x00027000);
-}
-// 16 bytes per lane from voff (per lane) + soff (the wave's) to LDS, in lane
-// order.
-__device__ inline void copy16(Rsrc r, unsigned voff, unsigned soff, uint8_t* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 16,
-                                           (int)voff, (int)soff, 0, 0);
-}
-__device__ inline void copy4(Rsrc r, unsigned voff, float* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)lds, 4,
-                                           (int)voff, 0, 0, 0);
-}
-// Waits until at most N of the wave's memory operations are under way (they
-// end in order; a barrier alone does not wait for copies to LDS).
-template <int N>
-__device__ inline void wait_memory() {
-  static_assert(N < 64, "six bits");
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
-}
-
-// Barrier of the block that leaves copies to LDS under way (the fence of
-// __syncthreads waits for every one): the wave's own LDS reads and writes are
-// done, and none of the compiler's is moved across.
-__device__ inline void block_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
 template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int EU_ = 2>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
@@ -310,49 +276,6 @@ struct Tile {
   static_assert(SM * WM * 32 == BM && SN * WN * 32 == BN, "whole sub-tiles");
   static_assert(AC * WAVES * 8 == BM && BC * WAVES * 8 == BN, "whole copies");
   static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
-};
-
-// The row tiles of the experts, found by every wave from expert_offsets: a
-// lane holds the tiles of E / 64 consecutive experts, a prefix sum over the
-// lanes places them.
-template <int BM>
-struct Spans {
-  int first, mine, per;  // tiles before this lane's experts, its own, experts per lane
-  __device__ inline int tiles(const Fp8MatmulArgs& g, int e) const {
-    return (g.expert_offsets[e + 1] - g.expert_offsets[e] + BM - 1) / BM;
-  }
-  __device__ inline int count(const Fp8MatmulArgs& g) {
-    const int lane = threadIdx.x & 63;
-    per = (g.E + 63) / 64;
-    mine = 0;
-    for (int i = 0; i < per; i++)
-      if (lane * per + i < g.E) mine += tiles(g, lane * per + i);
-    int sum = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int v = __shfl_up(sum, off, 64);
-      if (lane >= off) sum += v;
-    }
-    first = sum - mine;
-    return __builtin_amdgcn_readlane(sum, 63);
-  }
-  // Expert and rows [*m0, *mend) of row tile t (below count).
-  __device__ inline int find(const Fp8MatmulArgs& g, int t, int* m0, int* mend) const {
-    const unsigned long long at = __ballot(first <= t && t < first + mine);
-    const int lane = (int)__ffsll(at) - 1;
-    int left = t - __builtin_amdgcn_readlane(first, lane);
-    const int per_lane = __builtin_amdgcn_readfirstlane(per);
-    int e = lane * per_lane;
-    for (int i = 0; i + 1 < per_lane && left >= tiles(g, e); i++) left -= tiles(g, e++);
-    *m0 = g.expert_offsets[e] + left * BM;
-    *mend = min(*m0 + BM, g.expert_offsets[e + 1]);
-    return e;
-  }
-};
-
-template <int V>
-struct Int {
-  static constexpr int value = V;
 };
 
 // OUT32: out is fp32 (the sums of a K split, and fp32 outputs); EXACT: the

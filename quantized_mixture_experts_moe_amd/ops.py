@@ -34,7 +34,8 @@ EXPORTS = (
     "qmoe_decode", "qmoe_fp8_quant", "qmoe_fp8_matmul_workspace", "qmoe_fp8_matmul",
     "qmoe_fp8_grouped_matmul", "qmoe_balance_workspace", "qmoe_balance", "qmoe_balance_backward",
     "qmoe_pre_norm", "qmoe_post_norm", "qmoe_norm_backward_workspace", "qmoe_pre_norm_backward",
-    "qmoe_post_norm_backward",
+    "qmoe_post_norm_backward", "qmoe_grouped_matmul", "qmoe_grouped_wgrad_workspace",
+    "qmoe_grouped_wgrad", "qmoe_combine_backward", "qmoe_w4_matmul_workspace", "qmoe_w4_matmul",
 )
 # Forms in which pre_norm and post_norm write a norm (qmoe_form).
 NORM_FORMS = {"bf16": 0, "f32": 1, "int8": 2, "e4m3": 3, "e4m3_128": 4}
@@ -140,7 +141,17 @@ def _lib() -> ctypes.CDLL:
             ("qmoe_pre_norm_backward", ctypes.c_int,
              [vp, vp, i32, vp, f32, vp, i32, i32, vp, vp, vp, sz, vp]),
             ("qmoe_post_norm_backward", ctypes.c_int,
-             [vp, vp, i32, vp, vp, i32, f32, f32, i32, i32, vp, vp, vp, vp, vp, sz, vp])):
+             [vp, vp, i32, vp, vp, i32, f32, f32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+            ("qmoe_grouped_matmul", ctypes.c_int,
+             [vp, i32, vp, i32] + [vp] * 4 + [i32] * 7 + [vp, vp, i32, vp]),
+            ("qmoe_grouped_wgrad_workspace", sz, [i32] * 5),
+            ("qmoe_grouped_wgrad", ctypes.c_int,
+             [vp, vp, i32, vp, vp] + [i32] * 6 + [vp, i32, i32, vp, sz, vp]),
+            ("qmoe_combine_backward", ctypes.c_int,
+             [vp, vp, i32, vp, vp] + [i32] * 4 + [vp] * 5),
+            ("qmoe_w4_matmul_workspace", sz, [i32] * 3),
+            ("qmoe_w4_matmul", ctypes.c_int,
+             [vp] * 3 + [i32] * 6 + [vp, vp, i32, vp, sz, vp])):
         getattr(L, name).restype, getattr(L, name).argtypes = res, args
     _LIB = L
     return L
@@ -465,7 +476,8 @@ def decode_forward(scheme: str, logits: torch.Tensor, x: torch.Tensor,
 
 
 # ---------------------------------------------------------------- around the experts
-# Block-128 fp8 quantizer and products, balance loss, norms.  These check
+# Block-128 fp8 quantizer and products, the experts' bf16 products with their
+# gradients, 4-bit dense products, balance loss, norms.  These check
 # shapes, types and devices here (ValueError), since the C ABI sees pointers
 # only, and run on the current stream of the tensors' device.  None of them
 # records itself for autograd, whatever its arguments require: gradients are calls
@@ -658,9 +670,10 @@ def fp8_grouped_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor,
     return out
 
 
-# Tile height (align's block_m) for the block-128 fp8 expert products: they
-# take an expert's rows whatever the height, so the least padding is best.
-FP8_BLOCK_M = 16
+# Tile height (align's block_m) for the block-128 fp8 and the bf16 expert
+# products: they take an expert's rows whatever the height, so the least padding
+# is best.
+FP8_BLOCK_M = GROUPED_BLOCK_M = 16
 
 
 def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor, weights: dict,
@@ -682,6 +695,205 @@ def fp8_moe_forward(logits: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor
                                pair_rows=True)
         out, _ = combine(y, w)
     return {"topk_ids": ids, "topk_w": w, "align": al, "y_pairs": y, "out": out}
+
+
+# qmoe_act and qmoe_w4_format.
+ACTS = {None: 0, "silu_mul": 1, "silu_mul_backward": 2}
+W4_INT4, W4_MXFP4 = 0, 1
+
+
+def _list(al: dict, T: int, k: int, E: int):
+    """Checks align's (or route_align's) result for these sizes; returns block_m."""
+    bm = al["block_m"]
+    cap = align_capacity(T, k, E, bm)
+    _need(cap > 0 or T == 0, "bad sizes: T %d, k %d, E %d, block_m %d", T, k, E, bm)
+    _tensor(al["sorted_pair_ids"], "sorted_pair_ids", (cap,), torch.int32)
+    _tensor(al["tile_expert"], "tile_expert", (cap // bm,), torch.int32)
+    _tensor(al["expert_offsets"], "expert_offsets", (E + 1,), torch.int32)
+    _tensor(al["num_padded"], "num_padded", (1,), torch.int32)
+    return bm
+
+
+def _rows_of(x, name: str, k: int, pair_rows: bool) -> int:
+    """Tokens of bf16 rows [T, K] or [T*k, K]."""
+    _need(x.dim() == 2, "%s must have 2 axes", name)
+    _need(x.dtype == torch.bfloat16, "%s must be bfloat16, not %s", name, x.dtype)
+    _need(k >= 1 and (not pair_rows or x.shape[0] % k == 0),
+          "%d pair rows are not a multiple of k = %d", x.shape[0], k)
+    return x.shape[0] // k if pair_rows else x.shape[0]
+
+
+def grouped_matmul(a: torch.Tensor, b: torch.Tensor, al: dict, k: int, pair_rows: bool = False,
+                   trans: bool = False, act: Optional[str] = None,
+                   gu: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qmoe_grouped_matmul, bf16: row p of the result is a[row(p)] . b[e]^T (b
+    [E, N, K]) or, with trans, a[row(p)] . b[e] (b [E, K, N]: the gradient of
+    the rows), e the expert of pair p, row(p) = p // k (a [T, K]) or p
+    (pair_rows, a [T*k, K]); `al` is align's (or route_align's) result.
+    act="silu_mul" (b = gate | up rows): SiLU(g) * u [T*k, N/2]; gu, a bf16
+    tensor [T*k, N], receives g | u.  act="silu_mul_backward" (with trans):
+    the gradient of g | u [T*k, 2N] for the gradient a . b of SiLU(g) * u,
+    gu being what the forward call kept."""
+    _need(act in ACTS, "act must be one of %s, not %r", list(ACTS), act)
+    _need(b.dim() == 3, "b must be [E, N, K]")
+    E = b.shape[0]
+    N, K = (b.shape[2], b.shape[1]) if trans else (b.shape[1], b.shape[2])
+    T = _rows_of(a, "a", k, pair_rows)
+    _need(a.shape[1] == K, "a's rows have %d values, b's %d", a.shape[1], K)
+    _need(b.dtype == torch.bfloat16, "b must be bfloat16, not %s", b.dtype)
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    if act == "silu_mul":
+        _need(not trans and N % 2 == 0, "act='silu_mul' takes b [E, 2I, K] without trans")
+        cols, gcols = N // 2, N
+    elif act == "silu_mul_backward":
+        _need(trans and gu is not None, "act='silu_mul_backward' goes with trans and takes gu")
+        cols, gcols = 2 * N, 2 * N
+    else:
+        _need(gu is None, "gu goes with an act")
+        cols, gcols = N, 0
+    if gu is not None:
+        _tensor(gu, "gu", (T * k, gcols), torch.bfloat16)
+    bm = _list(al, T, k, E)
+    dev = _one_device(a, b, al["sorted_pair_ids"], al["tile_expert"], al["expert_offsets"],
+                      al["num_padded"], gu, out)
+    out = _out(out, (T * k, cols), out_dtype, dev)
+    _call(dev, "qmoe_grouped_matmul", _addr(a), int(pair_rows), _addr(b), int(trans),
+          _addr(al["sorted_pair_ids"]), _addr(al["tile_expert"]), _addr(al["expert_offsets"]),
+          _addr(al["num_padded"]), T, k, E, bm, N, K, ACTS[act], _addr(gu), _addr(out),
+          _float_kind(out, "out"))
+    return out
+
+
+def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, al: dict, k: int, pair_rows: bool = False,
+                  out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                  accumulate: bool = False, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qmoe_grouped_wgrad: [E, N, K], dw[e] the sum over e's pairs p of
+    dy[p]^T x[row(p)] (dy [T*k, N], x [T, K] or, with pair_rows, [T*k, K],
+    bf16): the gradient of grouped_matmul's b for the gradient dy of its out.
+    accumulate (fp32): added to ``out``."""
+    T = _rows_of(x, "x", k, pair_rows)
+    _need(dy.dim() == 2 and dy.shape[0] == T * k, "dy must have %d rows", T * k)
+    _need(dy.dtype == torch.bfloat16, "dy must be bfloat16, not %s", dy.dtype)
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    _need(not accumulate or (out is not None and out_dtype == torch.float32),
+          "accumulate takes an fp32 out")
+    E, N, K = al["expert_offsets"].shape[0] - 1, dy.shape[1], x.shape[1]
+    bm = _list(al, T, k, E)
+    dev = _one_device(dy, x, al["sorted_pair_ids"], al["tile_expert"], al["expert_offsets"],
+                      al["num_padded"], ws, out)
+    out = _out(out, (E, N, K), out_dtype, dev)
+    need = int(_lib().qmoe_grouped_wgrad_workspace(T, k, E, N, K))
+    if need and (ws is None or ws.numel() * ws.element_size() < need):
+        ws = _ws(need, dev)
+    _call(dev, "qmoe_grouped_wgrad", _addr(dy), _addr(x), int(pair_rows),
+          _addr(al["sorted_pair_ids"]), _addr(al["expert_offsets"]), T, k, E, bm, N, K, _addr(out),
+          _float_kind(out, "out"), int(accumulate), _addr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return out
+
+
+def combine_backward(dout: torch.Tensor, y_pairs: torch.Tensor, topk_ids: torch.Tensor,
+                     topk_w: torch.Tensor, E: int, add: Optional[torch.Tensor] = None) -> dict:
+    """qmoe_combine_backward: {"dy" [T*k, H], "dw" fp32 [T, k], "dlogits" fp32
+    [T, E]} for the gradient dout [T, H] of combine(y_pairs, topk_w) with
+    route's picks; add [T, E] is another gradient of the logits (a balance
+    loss'), added to dlogits."""
+    _need(dout.dim() == 2 and topk_w.dim() == 2, "dout must be [T, H] and topk_w [T, k]")
+    T, H = dout.shape
+    k = topk_w.shape[1]
+    dt = _float_kind(dout, "dout")
+    _tensor(y_pairs, "y_pairs", (T * k, H), dout.dtype)
+    _tensor(topk_w, "topk_w", (T, k), torch.float32)
+    _tensor(topk_ids, "topk_ids", (T, k), torch.int32)
+    if add is not None:
+        _tensor(add, "add", (T, E), torch.float32)
+    dev = _one_device(dout, y_pairs, topk_ids, topk_w, add)
+    r = {"dy": torch.empty_like(y_pairs), "dw": torch.empty_like(topk_w),
+         "dlogits": torch.empty((T, E), dtype=torch.float32, device=dev)}
+    _call(dev, "qmoe_combine_backward", _addr(dout), _addr(y_pairs), dt, _addr(topk_ids),
+          _addr(topk_w), T, k, H, E, _addr(add), r["dy"].data_ptr(), r["dw"].data_ptr(),
+          r["dlogits"].data_ptr())
+    return r
+
+
+def bf16_moe_forward(logits: torch.Tensor, x: torch.Tensor, weights: dict, k: int) -> dict:
+    """The layer with bf16 experts, as it is trained: route -> align -> gate/up
+    product with SiLU*mul -> down product -> combine.  x bf16 [T, H]; weights:
+    w13 [E, 2I, H] and w2 [E, H, I] bf16; H and I multiples of 8.  The result
+    holds what bf16_moe_backward needs."""
+    T, E = logits.shape
+    _need(x.shape[0] == T, "x has %d rows, logits %d", x.shape[0], T)
+    dev = _one_device(logits, x)
+    with torch.cuda.device(dev):
+        ids, w, al = route_align(logits, k, GROUPED_BLOCK_M)
+        gu = torch.empty((T * k, weights["w13"].shape[1]), dtype=torch.bfloat16, device=dev)
+        h = grouped_matmul(x, weights["w13"], al, k, act="silu_mul", gu=gu)
+        y = grouped_matmul(h, weights["w2"], al, k, pair_rows=True)
+        out, _ = combine(y, w)
+    return {"topk_ids": ids, "topk_w": w, "align": al, "gu": gu, "h": h, "y_pairs": y, "out": out}
+
+
+def bf16_moe_backward(dout: torch.Tensor, fwd: dict, x: torch.Tensor, weights: dict,
+                      add: Optional[torch.Tensor] = None,
+                      weight_dtype: torch.dtype = torch.float32) -> dict:
+    """Gradients of bf16_moe_forward's out (fwd is its result, x and weights its
+    inputs): {"dx" bf16 [T, H], "dlogits" fp32 [T, E] (+ add), "dw13", "dw2" in
+    weight_dtype}.  Between the calls values are rounded to bf16, as in the
+    forward pass."""
+    al, w, ids = fwd["align"], fwd["topk_w"], fwd["topk_ids"]
+    k, E = w.shape[1], weights["w13"].shape[0]
+    with torch.cuda.device(_one_device(dout, x)):
+        c = combine_backward(dout, fwd["y_pairs"], ids, w, E, add=add)
+        dw2 = grouped_wgrad(c["dy"], fwd["h"], al, k, pair_rows=True, out_dtype=weight_dtype)
+        dgu = grouped_matmul(c["dy"], weights["w2"], al, k, pair_rows=True, trans=True,
+                             act="silu_mul_backward", gu=fwd["gu"])
+        dw13 = grouped_wgrad(dgu, x, al, k, out_dtype=weight_dtype)
+        dxp = grouped_matmul(dgu, weights["w13"], al, k, pair_rows=True, trans=True)
+        dx, _ = combine(dxp, torch.ones_like(w))
+    return {"dx": dx, "dlogits": c["dlogits"], "dw13": dw13, "dw2": dw2}
+
+
+def w4_matmul_workspace(M: int, N: int, K: int) -> int:
+    return int(_lib().qmoe_w4_matmul_workspace(M, N, K))
+
+
+def w4_matmul(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+              act: Optional[str] = None, add: Optional[torch.Tensor] = None,
+              out_dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """qmoe_w4_matmul: x bf16 [M, K] times 4-bit weights [N, K] (codes uint8 [N,
+    K/2]) with a scale per group: fp16 [N, K/group], int4 codes, group 32, 64
+    or 128; or uint8 (e8m0) [N, K/32], e2m1 codes.  act="silu_mul": the weights
+    are gate | up rows, the result SiLU(g) * u [M, N/2].  add: a tensor of the
+    result's shape and type, added before the rounding (it may be ``out``)."""
+    _need(act in (None, "silu_mul"), "act must be None or 'silu_mul', not %r", act)
+    _need(x.dim() == 2 and codes.dim() == 2 and scale.dim() == 2,
+          "x, codes and scale must have 2 axes")
+    M, K = x.shape
+    N, groups = codes.shape[0], scale.shape[1]
+    _tensor(x, "x", (M, K), torch.bfloat16)
+    _tensor(codes, "codes", (N, K // 2), torch.uint8)
+    _tensor(scale, "scale", (N, groups), torch.float16, torch.uint8)
+    fmt = W4_INT4 if scale.dtype == torch.float16 else W4_MXFP4
+    _need(groups > 0 and K % groups == 0, "%d scales do not divide %d values", groups, K)
+    group = K // groups
+    _need(group in ((32, 64, 128) if fmt == W4_INT4 else (32,)),
+          "groups of %d values are not supported", group)
+    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
+    _need(act is None or N % 2 == 0, "act='silu_mul' takes an even number of weight rows")
+    cols = N // 2 if act else N
+    if add is not None:
+        _tensor(add, "add", (M, cols), out_dtype)
+    dev = _one_device(x, codes, scale, add, ws, out)
+    out = _out(out, (M, cols), out_dtype, dev)
+    need = w4_matmul_workspace(M, N, K)
+    if need and (ws is None or ws.numel() * ws.element_size() < need):
+        ws = _ws(need, dev)
+    _call(dev, "qmoe_w4_matmul", _addr(x), _addr(codes), _addr(scale), fmt, group, M, N, K,
+          ACTS[act], _addr(add), _addr(out), _float_kind(out, "out"), _addr(ws),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return out
 
 
 def _mask_ptr(mask, T: int):
