@@ -448,9 +448,7 @@ qmoe_status qmoe_fp8_grouped_matmul(const uint8_t* a, const float* a_scale, int3
  * qmoe_grouped_wgrad -- dw[e] = sum over e's pairs p of dy[p]^T x[row(p)],
  *   dw [E, N, K] bf16 or fp32, dy [T*k, N], x [T, K] or [T*k, K] as a above.
  *   Experts without pairs get zeros.  accumulate = 1 (fp32): added to what dw
- *   holds.  ws: qmoe_grouped_wgrad_workspace bytes (0: none needed, ws may be
- *   NULL), 256-byte aligned, contents need no initialisation; calls that share
- *   it must be ordered on one stream.                                       */
+ *   holds.                                                                  */
 typedef enum {
   QMOE_ACT_NONE = 0,
   QMOE_ACT_SILU_MUL = 1,
@@ -462,12 +460,11 @@ qmoe_status qmoe_grouped_matmul(const uint16_t* a, int32_t pair_rows, const uint
                                 const int32_t* num_padded, int32_t T, int32_t k, int32_t E,
                                 int32_t block_m, int32_t N, int32_t K, int32_t act, uint16_t* gu,
                                 void* out, int32_t out_dtype, void* stream);
-size_t qmoe_grouped_wgrad_workspace(int32_t T, int32_t k, int32_t E, int32_t N, int32_t K);
 qmoe_status qmoe_grouped_wgrad(const uint16_t* dy, const uint16_t* x, int32_t pair_rows,
                                const int32_t* sorted_pair_ids, const int32_t* expert_offsets,
                                int32_t T, int32_t k, int32_t E, int32_t block_m, int32_t N,
                                int32_t K, void* dw, int32_t out_dtype, int32_t accumulate,
-                               void* ws, size_t ws_bytes, void* stream);
+                               void* stream);
 
 /* ---------------------------------------------------------------------
  * qmoe_combine_backward -- the gradients of qmoe_combine's sum and of

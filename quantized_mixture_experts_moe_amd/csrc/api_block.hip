@@ -219,13 +219,11 @@ qmoe_status qmoe_grouped_matmul(const uint16_t* a, int32_t pair_rows, const uint
   return hip_status(launch_grouped_matmul(g, (hipStream_t)stream));
 }
 
-size_t qmoe_grouped_wgrad_workspace(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
-
 qmoe_status qmoe_grouped_wgrad(const uint16_t* dy, const uint16_t* x, int32_t pair_rows,
                                const int32_t* sorted_pair_ids, const int32_t* expert_offsets,
                                int32_t T, int32_t k, int32_t E, int32_t block_m, int32_t N,
                                int32_t K, void* dw, int32_t out_dtype, int32_t accumulate,
-                               void* ws, size_t ws_bytes, void* stream) {
+                               void* stream) {
   if (!valid_list(T, k, E, block_m) || N < 8 || K < 8 || pair_rows < 0 || pair_rows > 1 ||
       !valid_dtype(out_dtype) || accumulate < 0 || accumulate > 1 ||
       (accumulate && out_dtype != QMOE_DT_F32))

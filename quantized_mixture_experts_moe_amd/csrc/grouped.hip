@@ -32,6 +32,17 @@ __device__ inline int pair_of(const GroupedArgs& g, int slot) {
 }
 __device__ inline int a_row(const GroupedArgs& g, int p) { return g.pair_rows ? p : p / g.k; }
 
+// Four values past the L2, which is left to the operands.
+template <bool F32>
+__device__ inline void store4_past(void* p, size_t i, const float v[4]) {
+  if constexpr (F32)
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]},
+                                reinterpret_cast<f32x4*>(reinterpret_cast<float*>(p) + i));
+  else
+    __builtin_nontemporal_store(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])},
+                                reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(p) + i));
+}
+
 // SiLU(g) u's gradients for the gradient d of the product.  With t = exp(-|g|)
 // neither the sigmoid nor 1 minus it is a difference.
 __device__ inline void silu_mul_grad(float d, float g, float u, float* dg, float* du) {
@@ -164,17 +175,23 @@ __global__ __launch_bounds__(64 * KS) void grouped_rows_kernel(GroupedArgs g) {
 // width, and is turned on the way to registers by LDS's transposing read (four
 // rows x 16 columns per 16 lanes); the 32-byte units of a row are stored in the
 // order u ^ 2 (row % 4), so that the four rows lie in different banks.
-template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int EU_ = 2>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_, int EU_ = 2,
+          int SPREAD_ = 2, int STEPS_ = 4>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int EU = EU_;  // waves per SIMD that the registers allow for
+  static constexpr int SPREAD = SPREAD_;  // steps of a K block that issue the next one's copies
+  static constexpr int STEPS = STEPS_;    // steps of 16 values of K per K block
   static constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
   static constexpr int SM = BM / WM / 32, SN = BN / WN / 32;
-  static constexpr int AC = BM / 8 / WAVES, BC = BN / 8 / WAVES;  // copies per wave and K block
+  // copies of 1 KiB per wave and K block
+  static constexpr int AC = BM * STEPS / 32 / WAVES, BC = BN * STEPS / 32 / WAVES;
   static constexpr int COPIES = AC + BC;
-  static constexpr int B_AT = BM * 128, STAGE = B_AT + BN * 128;
+  static constexpr int B_AT = BM * STEPS * 32, STAGE = B_AT + BN * STEPS * 32;
+  static constexpr int FIT = 160 * 1024 / (STAGES * STAGE + WAVES * 4096 + 2 * BM * 4 + 1028 * 4);
+  static constexpr int PER_CU = FIT > 0 ? FIT : 1;  // blocks
   static_assert(SM * WM * 32 == BM && SN * WN * 32 == BN, "whole sub-tiles");
-  static_assert(AC * WAVES * 8 == BM && BC * WAVES * 8 == BN, "whole copies");
+  static_assert(AC * WAVES * 32 == BM * STEPS && BC * WAVES * 32 == BN * STEPS, "whole copies");
   static_assert(STAGES * STAGE <= 160 * 1024, "LDS");
 };
 
@@ -209,141 +226,211 @@ template <int V>
 struct Int {
   static constexpr int value = V;
 };
+constexpr int least(int a, int b) { return a < b ? a : b; }
 
-// The K loop: STAGES - 1 K blocks under way, copy(stage, kb, c) one of a K
-// block's COPIES copies of this wave (of nothing behind the last block),
-// compute(stage, next stage, kb) a K block, with the next one's copies in it.
-template <class C, class Copy, class Compute>
-__device__ inline void k_loop(uint8_t* lds, int KB, const Copy& copy, const Compute& compute) {
+// The time of a K block in stage st: the wave issues the matrix instructions of
+// the step before (the last one's of the block before at first; FIRST: there is
+// none), between them the reads of the next step and copies to stage nx, in the
+// order written here (the compiler would gather the reads of a step in front of it
+// and the copies behind).  copy(nx, c) issues one of the wave's COPIES copies;
+// read(st, s, r) one of the NR fragments of step s, to the half s % 2 of the
+// wave's; mul(s, m) one of the NM matrix instructions on them.  The last step's
+// are left to the next K block, or to the end.
+template <class C, int NR, int NM, bool FIRST, class Copy, class Read, class Mul>
+__device__ inline void k_block(const uint8_t* __restrict__ st, uint8_t* __restrict__ nx,
+                               const Copy& copy, const Read& read, const Mul& mul) {
+  constexpr int PER = (C::COPIES + C::SPREAD - 1) / C::SPREAD;  // copies per step
+#pragma unroll
+  for (int s = 0; s < C::STEPS; s++) {
+#pragma unroll
+    for (int m = 0; m < NM; m++) {
+      if (!FIRST || s > 0) mul((s + C::STEPS - 1) % C::STEPS, m);
+#pragma unroll
+      for (int r = 0; r < NR; r++)
+        if (r * NM / NR == m) read(st, s, r);
+#pragma unroll
+      for (int c = 0; c < PER; c++)
+        if (c * NM / PER == m && s * PER + c < C::COPIES) copy(nx, s * PER + c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// The K loop of a block with one tile, STAGES - 1 K blocks under way: copy(stage,
+// kb, c) is of nothing behind the last block.
+template <class C, int NR, int NM, class Copy, class Read, class Mul>
+__device__ inline void k_loop(uint8_t* lds, int KB, const Copy& copy, const Read& read,
+                              const Mul& mul) {
 #pragma unroll
   for (int s = 0; s < C::STAGES - 1; s++)
 #pragma unroll
     for (int u = 0; u < C::COPIES; u++) copy(lds + s * C::STAGE, s, u);
-  for (int kb = 0; kb < KB;) {
-#pragma unroll
-    for (int s = 0; s < C::STAGES; s++) {
-      if (kb >= KB) continue;
-      // Stage s has landed (the stages behind it may be under way), in every
-      // wave; and every wave is done with the stage before, which is free now.
+  if (KB > 0) {
+    // The block's stage has landed (those behind it may be under way), in every
+    // wave; and every wave is done with the stage before, which is free now.
+    auto step = [&](auto first, uint8_t* st, uint8_t* nx, int kb) {
       wait_memory<(C::STAGES - 2) * C::COPIES>();
       block_barrier();
-      compute(lds + s * C::STAGE, lds + (s + C::STAGES - 1) % C::STAGES * C::STAGE, kb);
-      kb++;
+      k_block<C, NR, NM, decltype(first)::value != 0>(
+          st, nx, [&](uint8_t* to, int c) { copy(to, kb + C::STAGES - 1, c); }, read, mul);
+    };
+    step(Int<1>{}, lds, lds + (C::STAGES - 1) * C::STAGE, 0);
+    uint8_t *nx = lds, *st = lds + C::STAGE;
+    for (int kb = 1; kb < KB; kb++) {
+      step(Int<0>{}, st, nx, kb);
+      nx = st;
+      st = st == lds + (C::STAGES - 1) * C::STAGE ? lds : st + C::STAGE;
     }
+#pragma unroll
+    for (int m = 0; m < NM; m++) mul(C::STEPS - 1, m);
   }
   wait_memory<0>();  // no copy is under way when LDS is used again, or ends
 }
 
-// A wave's 32 rows x SN 32 columns of sums, turned over in LDS so that
-// consecutive lanes hold consecutive bytes of a row (the 16-byte pieces of a
-// row in the order p ^ row % 8, against bank conflicts).  value(i, r): the
-// lane's sum r of sub-tile i; then piece(row, byte, address) for 16 bytes each.
-template <int SN, bool F32, class Value, class Piece>
+// 32 rows x 8 NQ columns of a wave's sums (NQ at most ROW bytes of them), turned
+// over in LDS so that consecutive lanes hold consecutive bytes of a row.  The
+// 16-byte pieces of a row lie in an order that changes from row to row (every row
+// where 128 bytes or more make a row, every fourth of 64 bytes), against bank
+// conflicts.  value(q, r): the lane's value of column 8 q + 4 h + r, h its half;
+// then piece(u, byte, address) for 16 bytes of row u * 64 / (ROW / 16) + lane / (ROW
+// / 16).
+template <int NQ, bool F32, int ROW, class Value, class Piece>
 __device__ inline void turn_over(uint8_t* mine, const Value& value, const Piece& piece) {
-  constexpr int EB = F32 ? 4 : 2, RB = SN * 32 * EB, PIECES = RB / 16, RPI = 64 / PIECES;
+  constexpr int EB = F32 ? 4 : 2, PIECES = ROW / 16, RPI = 64 / PIECES;
+  static_assert(NQ * 8 * EB <= ROW, "a row's bytes");
   const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
+  auto order = [](int row) { return (ROW >= 128 ? row : ROW >= 64 ? row >> 2 : row >> 3) & 7 & (PIECES - 1); };
 #pragma unroll
-  for (int i = 0; i < SN; i++)
-#pragma unroll
-    for (int q = 0; q < 4; q++) {
-      const int byte = (i * 32 + 8 * q + 4 * h) * EB;
-      uint8_t* d = mine + r32 * RB + ((byte / 16) ^ (r32 % 8 % PIECES)) * 16 + byte % 16;
-      const float v[4] = {value(i, 4 * q), value(i, 4 * q + 1), value(i, 4 * q + 2),
-                          value(i, 4 * q + 3)};
-      store4<F32>(d, 0, v);
-    }
+  for (int q = 0; q < NQ; q++) {
+    const int byte = (8 * q + 4 * h) * EB;
+    uint8_t* d = mine + r32 * ROW + ((byte / 16) ^ order(r32)) * 16 + byte % 16;
+    const float v[4] = {value(q, 0), value(q, 1), value(q, 2), value(q, 3)};
+    store4<F32>(d, 0, v);
+  }
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int u = 0; u < 32 / RPI; u++) {
     const int row = u * RPI + lane / PIECES, at = lane % PIECES;
-    piece(u, row, at * 16, mine + row * RB + (at ^ (row % 8 % PIECES)) * 16);
+    if (at * 16 < NQ * 8 * EB) piece(u, at * 16, mine + row * ROW + (at ^ order(row)) * 16);
   }
   __builtin_amdgcn_wave_barrier();
 }
 
 // out of every expert.  TRANS: b is [E,K,N] (turned).
+//
+// A block takes one tile after another.  While it works on a tile's last K block
+// the next tile's first one is on its way, and the finished sums go to memory
+// under the next tile's second one, so that neither a tile's start nor its end
+// leaves the memory idle (128 experts of 1536 x 2048, 2048 tokens: 232 us with a
+// block per tile).
 template <class C, bool TRANS, int ACT, bool F32>
 __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(GroupedArgs g) {
   constexpr int SM = C::SM, SN = C::SN;
-  static_assert(ACT != kSilu || (SN % 2 == 0 && !TRANS), "gate and up sub-tiles");
+  static_assert(C::STAGES == 2 && C::STEPS == 4, "two stages of 64 values");
+  static_assert(ACT != kSilu || (!TRANS && SN % 2 == 0), "a projection, 32 columns of out");
   static_assert(ACT != kSiluGrad || TRANS, "the gradient's way back");
-  __shared__ __align__(1024) uint8_t lds[C::STAGES * C::STAGE];
+  static_assert(C::BM <= C::THREADS, "a thread per row");
+  // Sums are turned over 32 rows x ROW bytes at a time, 128 where that fits into LDS.
+  constexpr bool WIDE = F32 || ACT == kSiluGrad;  // in fp32 (the gradient's are rounded behind)
+  constexpr int STAGED = C::STAGES * C::STAGE, PAIRS = 2 * C::BM * 4 + 1028 * 4;
+  constexpr int ROW = STAGED + C::WAVES * 4096 + PAIRS > 160 * 1024 ||
+                              (ACT == kSilu && !F32 && SN < 4) ? 64 : 128;
+  constexpr int ROOM = 32 * ROW;
+  static_assert(STAGED + C::WAVES * ROOM + PAIRS <= 160 * 1024, "LDS");
+  __shared__ __align__(1024) uint8_t lds[STAGED + C::WAVES * ROOM + PAIRS];
+  uint8_t* const turn = lds + C::STAGES * C::STAGE;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wm = wave % C::WM, wn = wave / C::WM;
+  uint8_t* const mine = turn + wave * ROOM;
+  // The tile's pairs, and the next one's.
+  int32_t* pairs = reinterpret_cast<int32_t*>(turn + C::WAVES * ROOM);
+  int32_t* next_pairs = pairs + C::BM;
+  // expert_offsets (a look-up in memory would wait behind the stores of a tile).
+  struct {
+    int32_t* expert_offsets;
+    int E;
+  } list = {pairs + 2 * C::BM, g.E};
+  for (int e = threadIdx.x; e <= g.E; e += C::THREADS) list.expert_offsets[e] = g.expert_offsets[e];
+  __syncthreads();
   // With SiLU * mul a tile is BN / 2 gate rows of b and the BN / 2 up rows of
-  // the same columns, in alternating sub-tiles of 32.
+  // the same columns, eight of each in turn, so that a lane holds both sums.
   constexpr int TN = ACT == kSilu ? C::BN / 2 : C::BN;
   const int cols = ACT == kSilu ? g.N / 2 : g.N;
-  const int ntn = (cols + TN - 1) / TN;
+  const int ntn = (cols + TN - 1) / TN, KB = (g.K + 63) / 64;
   Spans<C::BM> spans;
-  const int ntm = spans.count(g);
-  // The launch order deals blocks to the XCDs in turn: give each XCD a
+  const int ntm = spans.count(list);
+  // The launch order deals blocks to the XCDs in turn: each XCD's blocks take a
   // contiguous run of tiles, column-tile by column-tile inside bands of kBand
   // row tiles, so that its L2 sees the same rows again.
   constexpr int kBand = 8;
-  const int total = ntn * ntm, per = (total + 7) / 8;
-  const int id = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-  if (id >= total || (int)(blockIdx.x / 8) >= per) return;  // also past the tiles in use
-  const int band = id / (kBand * ntn), in = id - band * kBand * ntn;
-  const int rows = min(kBand, ntm - band * kBand);
-  const int mt = band * kBand + in % rows, n0 = in / rows * TN;
-  int m0, mend;
-  const int e = spans.find(g, mt, &m0, &mend);
-  const uint16_t* b = g.b + (size_t)e * g.N * g.K;
-  const int KB = (g.K + 63) / 64;
-  auto out_row = [&](int slot) { return slot < mend ? pair_of(g, slot) : -1; };
-  // The wave's sub-tiles of rows are wm, wm + WM, ...; those behind the last
-  // one with a row (an expert's rows stand in front of its padding) are left
-  // out.
-  int live = 0;
-#pragma unroll
-  for (int s = 0; s < SM; s++)
-    if (__ballot(out_row(m0 + (s * C::WM + wm) * 32 + (lane & 31)) >= 0) != 0) live = s + 1;
-  live = __builtin_amdgcn_readfirstlane(live);
+  const int total = ntn * ntm, per = (total + 7) / 8, stride = gridDim.x / 8;
+  const int last = min(total, ((int)(blockIdx.x % 8) + 1) * per);
+  int id = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  if (id >= last) return;  // also past the tiles in use
 
-  // Copies of a straight operand: 8 lanes per row, the rows of a wave's copy t
-  // being 8 t .. 8 t + 7; the chunk order alternates with t.
+  // A tile: expert e, rows from slot m0 to mend, columns from n0.
+  struct Where {
+    int e, m0, mend, n0;
+  };
+  auto find = [&](int at) {
+    Where w;
+    const int band = at / (kBand * ntn), in = at - band * kBand * ntn;
+    const int rows = min(kBand, ntm - band * kBand);
+    w.n0 = in / rows * TN;
+    w.e = spans.find(list, band * kBand + in % rows, &w.m0, &w.mend);
+    return w;
+  };
+  auto my_pair = [&](const Where& w) {
+    const int slot = w.m0 + (int)threadIdx.x;
+    return threadIdx.x < C::BM && slot < w.mend ? pair_of(g, slot) : -1;
+  };
+  // What the block copies: rows of a (byte offsets, behind every buffer where
+  // there is none), and b from the tile's first row or column.
   const unsigned rowb = 2u * (unsigned)g.K;  // bytes per straight row
-  const unsigned swz[2] = {16u * ((lane & 7) ^ ((lane >> 4) & 7)),
-                           16u * ((lane & 7) ^ ((4 + (lane >> 4)) & 7))};
   const size_t abytes = (size_t)g.Ma * rowb;
   unsigned av[C::AC];
+  Where at;
+  auto set_rows = [&](const int32_t* of) {
 #pragma unroll
-  for (int i = 0; i < C::AC; i++) {
-    const int p = out_row(m0 + (wave * C::AC + i) * 8 + (lane >> 3));
-    // no row: behind every buffer, so nothing is read
-    av[i] = p < 0 ? kNowhere : (unsigned)a_row(g, p) * rowb;
-  }
+    for (int i = 0; i < C::AC; i++) {
+      const int p = of[(wave * C::AC + i) * 8 + (lane >> 3)];
+      av[i] = p < 0 ? kNowhere : (unsigned)a_row(g, p) * rowb;
+    }
+  };
+  // Copies of a straight operand: 8 lanes per row, the rows of a wave's copy t
+  // being 8 t .. 8 t + 7; the chunk order alternates with t.
+  const unsigned swz[2] = {16u * ((lane & 7) ^ ((lane >> 4) & 7)),
+                           16u * ((lane & 7) ^ ((4 + (lane >> 4)) & 7))};
+  // Copy c of K block kb of the tile `at`, of nothing behind the last block.
   auto copy = [&](uint8_t* st, int kb, int c) {
-    const bool any = kb < KB;
-    const unsigned at = any ? kb * 128 : 0, left = rowb - at;  // bytes of the row from here
+    const unsigned any = kb < KB ? 1 : 0;
+    const unsigned from = any * kb * 128, left = rowb - from;  // bytes of the row from here
+    const uint16_t* const b = g.b + (size_t)at.e * g.N * g.K;
     if (c < C::AC) {
       const int t = wave * C::AC + c;
       const unsigned ch = swz[(C::AC % 2 == 0 ? c : t) & 1];
       // chunks behind the row's end are zeros
       const unsigned v = ch < left && av[c] != kNowhere ? av[c] + ch : kNowhere;
-      copy16(rsrc(g.a, any ? abytes : 0), v, at, st + t * 1024);
+      copy16(rsrc(g.a, abytes * any), v, from, st + t * 1024);
     } else if constexpr (TRANS) {
       typedef Turned<C::BN> Tn;
       const int t = wave * C::BC + (c - C::AC);
-      const uint16_t* base = b + (any ? (size_t)kb * 64 * g.N : 0) + n0;
-      const size_t bytes = any ? ((size_t)(g.K - kb * 64) * g.N - n0) * 2 : 0;
-      copy16(rsrc(base, bytes),
+      const int k0 = any * kb * 64;
+      copy16(rsrc(b + (size_t)k0 * g.N + at.n0, ((size_t)(g.K - k0) * g.N - at.n0) * 2 * any),
              2u * ((unsigned)Tn::row(t, lane) * (unsigned)g.N + (unsigned)Tn::col(t, lane)), 0,
              st + C::B_AT + t * 1024);
     } else {
       const int i = c - C::AC, t = wave * C::BC + i;
       const unsigned ch = swz[(C::BC % 2 == 0 ? i : t) & 1];
-      int row = t * 8, first = n0;
+      int row = t * 8, first = at.n0;
       if constexpr (ACT == kSilu) {
-        row = t / 8 * 32 + t % 4 * 8;
-        first += (t / 4 & 1) * cols;
+        row = t / 2 * 8;
+        first += (t & 1) * cols;
       }
-      const Rsrc rb = rsrc(b + (size_t)first * g.K,
-                           any && first < g.N ? (size_t)(g.N - first) * rowb : 0);
       const unsigned v = (unsigned)(row + (lane >> 3)) * rowb + ch;
-      copy16(rb, ch < left ? v : kNowhere, at, st + C::B_AT + t * 1024);
+      copy16(rsrc(b + (size_t)first * g.K, (size_t)(max(g.N - first, 0) * any) * rowb),
+             ch < left ? v : kNowhere, from, st + C::B_AT + t * 1024);
     }
   };
   // Reads: lane's row in a sub-tile and its half of each 16 values of K.
@@ -358,124 +445,184 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
   auto straight = [&](const uint8_t* t, int sub, int s) {
     return as_bf16(*reinterpret_cast<const u32x4*>(t + sub * 4096 + off[s]));
   };
-  f32x16 acc[SN][SM];
+
+  constexpr int PIECES = ROW / 16, RPI = 64 / PIECES;
+  // A lane holds four times four consecutive columns of its row per sub-tile; 32
+  // rows x ROW bytes of them are turned over in LDS at a time, so that consecutive
+  // lanes store consecutive bytes.
+  auto write_out = [&](f32x16 (&acc)[SN][SM], int live, int n0) {
+    constexpr int EB = F32 ? 4 : 2, NQ = ROW / (WIDE ? 32 : 16);  // eights of columns per turn
+    uint8_t* const out = reinterpret_cast<uint8_t*>(g.out);
 #pragma unroll
-  for (int i = 0; i < SN; i++)
+    for (int s = 0; s < SM; s++) {
+      if (s >= live) break;
+      int row[32 / RPI];
+#pragma unroll
+      for (int u = 0; u < 32 / RPI; u++)
+        row[u] = pairs[(s * C::WM + wm) * 32 + u * RPI + lane / PIECES];
+      // The lane's sums of sub-tile row s: columns 8 q + 4 h + r of the wave's.
+      auto sum = [&](int q, int r) { return acc[q / 4][s][4 * (q % 4) + r]; };
+      auto put = [&](uint8_t* to, int width, int u, int n, const uint8_t* v) {
+        const int p = row[u];
+        if (p >= 0 && n < cols)
+          __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(v),
+                                      reinterpret_cast<u32x4*>(to + (size_t)p * width));
+      };
+      if constexpr (ACT == kPlain) {
+        constexpr int Q = least(4 * SN, NQ);
+#pragma unroll
+        for (int q0 = 0; q0 < 4 * SN; q0 += Q)
+          turn_over<Q, F32, ROW>(
+              mine, [&](int q, int r) { return sum(q0 + q, r); },
+              [&](int u, int byte, const uint8_t* v) {
+                const int n = n0 + wn * SN * 32 + q0 * 8 + byte / EB;
+                put(out + (size_t)n * EB, cols * EB, u, n, v);
+              });
+      } else if constexpr (ACT == kSilu) {
+        const int nw = n0 + wn * SN * 16;  // the wave's first column of out
+        if (g.gu != nullptr) {
+          constexpr int Q = least(2 * SN, ROW / 16);
+#pragma unroll
+          for (int up = 0; up < 2; up++)
+#pragma unroll
+            for (int q0 = 0; q0 < 2 * SN; q0 += Q)
+              turn_over<Q, false, ROW>(
+                  mine, [&](int q, int r) { return sum(2 * (q0 + q) + up, r); },
+                  [&](int u, int byte, const uint8_t* v) {
+                    const int n = nw + q0 * 8 + byte / 2;
+                    put(reinterpret_cast<uint8_t*>(g.gu + up * cols + n), g.N * 2, u, n, v);
+                  });
+        }
+        constexpr int Q = least(2 * SN, NQ);
+#pragma unroll
+        for (int q0 = 0; q0 < 2 * SN; q0 += Q)
+          turn_over<Q, F32, ROW>(
+              mine,
+              [&](int q, int r) { return silu_mul(sum(2 * (q0 + q), r), sum(2 * (q0 + q) + 1, r)); },
+              [&](int u, int byte, const uint8_t* v) {
+                const int n = nw + q0 * 8 + byte / EB;
+                put(out + (size_t)n * EB, cols * EB, u, n, v);
+              });
+      } else {
+#pragma unroll
+        for (int q0 = 0; q0 < 4 * SN; q0 += NQ)
+          turn_over<NQ, true, ROW>(
+              mine, [&](int q, int r) { return sum(q0 + q, r); },
+              [&](int u, int byte, const uint8_t* v) {
+                const int n = n0 + wn * SN * 32 + q0 * 8 + byte / 4, p = row[u];
+                if (p < 0 || n >= cols) return;
+                const f32x4 d = *reinterpret_cast<const f32x4*>(v);
+                const size_t o2 = (size_t)p * 2 * cols + n;
+                const u32x2 gt = *reinterpret_cast<const u32x2*>(g.gu + o2);
+                const u32x2 up = *reinterpret_cast<const u32x2*>(g.gu + o2 + cols);
+                float dg[4], du[4];
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                  silu_mul_grad(d[r], bf16_f32((uint16_t)(gt[r / 2] >> (16 * (r & 1)))),
+                                bf16_f32((uint16_t)(up[r / 2] >> (16 * (r & 1)))), &dg[r], &du[r]);
+                store4_past<F32>(g.out, o2, dg);
+                store4_past<F32>(g.out, o2 + cols, du);
+              });
+      }
+    }
+  };
+
+  // The first tile's pairs, and its first K block.
+  at = find(id);
+  {
+    const int p = my_pair(at);
+    if (threadIdx.x < C::BM) pairs[threadIdx.x] = p;
+  }
+  __syncthreads();
+  set_rows(pairs);
+  uint8_t *st = lds, *nx = lds + C::STAGE;
+#pragma unroll
+  for (int u = 0; u < C::COPIES; u++) copy(st, 0, u);
+  // Block 0 has landed, in every wave, and the stage of the block before it is free:
+  // block 1 is copied there.
+  auto second = [&] {
+    wait_memory<0>();
+    block_barrier();
+    if (KB > 1) {
+#pragma unroll
+      for (int u = 0; u < C::COPIES; u++) copy(nx, 1, u);
+    }
+  };
+  second();
+  for (;;) {
+    const bool more = id + stride < last;
+    const Where next = more ? find(id + stride) : at;
+    const int p = more ? my_pair(next) : -1, n0 = at.n0;
+    // The wave's sub-tiles of rows are wm, wm + WM, ...; those behind the last one
+    // with a row (an expert's rows stand in front of its padding) are left out.
+    int live = 0;
 #pragma unroll
     for (int s = 0; s < SM; s++)
+      if (__ballot(pairs[(s * C::WM + wm) * 32 + r32] >= 0) != 0) live = s + 1;
+    live = __builtin_amdgcn_readfirstlane(live);
+    auto run = [&](auto live_) {
+      constexpr int LIVE = decltype(live_)::value;  // sub-tile rows to compute
+      f32x16 acc[SN][SM];
 #pragma unroll
-      for (int r = 0; r < 16; r++) acc[i][s][r] = 0.f;
-  auto run = [&](auto live_) {
-    constexpr int LIVE = decltype(live_)::value;  // sub-tile rows to compute
-    k_loop<C>(lds, KB, copy, [&](const uint8_t* st, uint8_t* nx, int kb) {
-      const int next = kb + C::STAGES - 1;
+      for (int i = 0; i < SN; i++)
 #pragma unroll
-      for (int s = 0; s < 4; s++) {
-        bf16x8 bf[SN], af[SM];
-        if constexpr (LIVE > 0) {
+        for (int s = 0; s < SM; s++)
 #pragma unroll
-          for (int i = 0; i < SN; i++) {
-            if constexpr (TRANS)
-              bf[i] = Turned<C::BN>::frag(st + C::B_AT, offb[i], s);
-            else
-              bf[i] = straight(st + C::B_AT, wn * SN + i, s);
-          }
-#pragma unroll
-          for (int j = 0; j < LIVE; j++) af[j] = straight(st, j * C::WM + wm, s);
+          for (int r = 0; r < 16; r++) acc[i][s][r] = 0.f;
+      bf16x8 bf[2][SN], af[2][LIVE];
+      auto read = [&](const uint8_t* t, int s, int r) {
+        if (r >= SN)
+          af[s & 1][r - SN] = straight(t, (r - SN) * C::WM + wm, s);
+        else if constexpr (TRANS)
+          bf[s & 1][r] = Turned<C::BN>::frag(t + C::B_AT, offb[r], s);
+        else
+          bf[s & 1][r] = straight(t + C::B_AT, wn * SN + r, s);
+      };
+      auto mul = [&](int s, int m) {
+        const int j = m / SN, i = m % SN;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[s & 1][i], af[s & 1][j], acc[i][j],
+                                                            0, 0, 0);
+      };
+      constexpr int NR = SN + LIVE, NM = SN * LIVE;
+      k_block<C, NR, NM, true>(st, nx, [](uint8_t*, int) {}, read, mul);
+      int from = 1;
+      for (int kb = 1; kb < KB; kb++) {
+        wait_memory<0>();
+        block_barrier();
+        uint8_t* const t = nx;
+        nx = st;
+        st = t;
+        if (kb == 1 && more && threadIdx.x < C::BM) next_pairs[threadIdx.x] = p;
+        from = kb + 1;
+        if (from == KB && more) {  // the next tile's first block
+          if (KB == 2) __syncthreads();
+          at = next;
+          set_rows(next_pairs);
+          from = 0;
         }
-#pragma unroll
-        for (int u = s * C::COPIES / 4; u < (s + 1) * C::COPIES / 4; u++) copy(nx, next, u);
-        if constexpr (LIVE > 0) {
-#pragma unroll
-          for (int j = 0; j < LIVE; j++)
-#pragma unroll
-            for (int i = 0; i < SN; i++)
-              acc[i][j] =
-                  __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[i], af[j], acc[i][j], 0, 0, 0);
-        }
+        k_block<C, NR, NM, false>(
+            st, nx, [&](uint8_t* to, int c) { copy(to, from, c); }, read, mul);
       }
-    });
-  };
-  switch (live) {  // (the same number of barriers in every one)
-    case 0: run(Int<0>{}); break;
-    case 1: run(Int<1>{}); break;
-    case 2: if constexpr (SM >= 2) run(Int<2>{}); break;
-    case 3: if constexpr (SM >= 3) run(Int<3>{}); break;
-    default: if constexpr (SM >= 4) run(Int<4>{}); break;
-  }
-
-  // A lane holds four times four consecutive columns of its row per sub-tile.
-  constexpr bool WIDE = F32 || ACT == kSiluGrad;  // turned over in fp32
-  constexpr int EB = F32 ? 4 : 2, RB = SN * 32 * (WIDE ? 4 : 2);
-  constexpr int RPI = 64 / (RB / 16);
-  static_assert(C::WAVES * 32 * RB <= (int)sizeof(lds), "every wave has room for 32 rows");
-  uint8_t* const out = reinterpret_cast<uint8_t*>(g.out);
-  __syncthreads();  // the last K block has been read
-  uint8_t* const mine = lds + wave * 32 * RB;
-  // Global column of byte `byte` of a turned row of values of W bytes, whose
-  // sub-tiles lie `step` columns apart.
 #pragma unroll
-  for (int s = 0; s < SM; s++) {
-    if (s >= live) break;
-    const int base = m0 + (s * C::WM + wm) * 32;
-    int orow[32 / RPI];
-#pragma unroll
-    for (int u = 0; u < 32 / RPI; u++) orow[u] = out_row(base + u * RPI + lane / (RB / 16));
-    if constexpr (ACT == kPlain) {
-      turn_over<SN, F32>(
-          mine, [&](int i, int r) { return acc[i][s][r]; },
-          [&](int u, int, int byte, const uint8_t* v) {
-            const int n = n0 + wn * SN * 32 + byte / EB;
-            if (orow[u] >= 0 && n < cols)
-              *reinterpret_cast<u32x4*>(out + ((size_t)orow[u] * cols + n) * EB) =
-                  *reinterpret_cast<const u32x4*>(v);
-          });
-    } else if constexpr (ACT == kSilu) {
-      if (g.gu != nullptr) {
-        constexpr int RPG = 64 / (SN * 4);  // rows per store of bf16 pieces
-        int grow[32 / RPG];
-#pragma unroll
-        for (int u = 0; u < 32 / RPG; u++) grow[u] = out_row(base + u * RPG + lane / (SN * 4));
-        turn_over<SN, false>(
-            mine, [&](int i, int r) { return acc[i][s][r]; },
-            [&](int u, int, int byte, const uint8_t* v) {
-              const int i = byte / 64, n = n0 + (wn * SN + i) / 2 * 32 + byte % 64 / 2;
-              if (grow[u] >= 0 && n < cols)
-                *reinterpret_cast<u32x4*>(g.gu + (size_t)grow[u] * g.N + (i & 1) * cols + n) =
-                    *reinterpret_cast<const u32x4*>(v);
-            });
-      }
-      constexpr int PH = SN / 2 * 32 * EB / 16, RPH = 64 / PH;
-      int hrow[32 / RPH];
-#pragma unroll
-      for (int u = 0; u < 32 / RPH; u++) hrow[u] = out_row(base + u * RPH + lane / PH);
-      turn_over<SN / 2, F32>(
-          mine, [&](int i, int r) { return silu_mul(acc[2 * i][s][r], acc[2 * i + 1][s][r]); },
-          [&](int u, int, int byte, const uint8_t* v) {
-            const int n = n0 + wn * SN * 16 + byte / EB;
-            if (hrow[u] >= 0 && n < cols)
-              *reinterpret_cast<u32x4*>(out + ((size_t)hrow[u] * cols + n) * EB) =
-                  *reinterpret_cast<const u32x4*>(v);
-          });
-    } else {
-      turn_over<SN, true>(
-          mine, [&](int i, int r) { return acc[i][s][r]; },
-          [&](int u, int, int byte, const uint8_t* v) {
-            const int n = n0 + wn * SN * 32 + byte / 4;
-            if (orow[u] < 0 || n >= cols) return;
-            const f32x4 d = *reinterpret_cast<const f32x4*>(v);
-            const uint16_t* gu = g.gu + (size_t)orow[u] * 2 * cols + n;
-            const u32x2 gt = *reinterpret_cast<const u32x2*>(gu);
-            const u32x2 up = *reinterpret_cast<const u32x2*>(gu + cols);
-            float dg[4], du[4];
-#pragma unroll
-            for (int r = 0; r < 4; r++)
-              silu_mul_grad(d[r], bf16_f32((uint16_t)(gt[r / 2] >> (16 * (r & 1)))),
-                            bf16_f32((uint16_t)(up[r / 2] >> (16 * (r & 1)))), &dg[r], &du[r]);
-            store4<F32>(g.out, (size_t)orow[u] * 2 * cols + n, dg);
-            store4<F32>(g.out, (size_t)orow[u] * 2 * cols + cols + n, du);
-          });
+      for (int m = 0; m < NM; m++) mul(3, m);
+      uint8_t* const t = nx;
+      nx = st;
+      st = t;
+      if (more) second();
+      write_out(acc, live, n0);
+    };
+    switch (live) {  // (the same number of barriers in every one)
+      case 0:
+      case 1: run(Int<1>{}); break;
+      case 2: run(Int<SM < 2 ? SM : 2>{}); break;
+      case 3: run(Int<SM < 3 ? SM : 3>{}); break;
+      default: run(Int<SM < 4 ? SM : 4>{}); break;
     }
+    if (!more) break;
+    int32_t* const t = pairs;
+    pairs = next_pairs;
+    next_pairs = t;
+    id += stride;
   }
 }
 
@@ -500,39 +647,52 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradA
   const int e = id / (ntn * ntm), in = id - e * ntn * ntm;
   const int n0 = in % ntm * C::BM, k0 = in / ntm * C::BN;
   const int first = g.expert_offsets[e], end = g.expert_offsets[e + 1];
-  const int KB = (end - first + 63) / 64;
+  constexpr int KROWS = 16 * C::STEPS;  // pairs per K block
+  const int KB = (end - first + KROWS - 1) / KROWS;
   const size_t dbytes = (size_t)g.P * g.N * 2, xbytes = (size_t)g.Mx * g.K * 2;
   // The copies' rows are pairs of the list, looked up one K block before they
   // are copied.
   int pa[C::AC], pb[C::BC];
+  unsigned va[C::AC], vb[C::BC];
   auto look = [&](int kb) {
 #pragma unroll
     for (int i = 0; i < C::AC; i++) {
-      const int slot = first + kb * 64 + Ta::row(wave * C::AC + i, lane);
+      const int slot = first + kb * KROWS + Ta::row(wave * C::AC + i, lane);
       pa[i] = slot < end ? g.sorted[slot] : g.P;
     }
 #pragma unroll
     for (int i = 0; i < C::BC; i++) {
-      const int slot = first + kb * 64 + Tb::row(wave * C::BC + i, lane);
+      const int slot = first + kb * KROWS + Tb::row(wave * C::BC + i, lane);
       pb[i] = slot < end ? g.sorted[slot] : g.P;
     }
   };
+  // (Called for K blocks in order, copy 0 first; the look-up of the next block's
+  // rows is under way before the copies.)
+  look(0);
   auto copy = [&](uint8_t* st, int kb, int c) {
-    if (c == 0) look(kb);
-    if (c < C::AC) {
-      const int t = wave * C::AC + c, col = n0 + Ta::col(t, lane);
-      const unsigned v = (unsigned)pa[c] < (unsigned)g.P && col < g.N
-                             ? 2u * ((unsigned)pa[c] * (unsigned)g.N + (unsigned)col)
-                             : kNowhere;
-      copy16(rsrc(g.dy, dbytes), v, 0, st + t * 1024);
-    } else {
-      const int i = c - C::AC, t = wave * C::BC + i, col = k0 + Tb::col(t, lane);
-      const int row = g.pair_rows ? pb[i] : pb[i] / g.k;
-      const unsigned v = (unsigned)pb[i] < (unsigned)g.P && col < g.K
-                             ? 2u * ((unsigned)row * (unsigned)g.K + (unsigned)col)
-                             : kNowhere;
-      copy16(rsrc(g.x, xbytes), v, 0, st + C::B_AT + t * 1024);
+    if (c == 0) {
+#pragma unroll
+      for (int i = 0; i < C::AC; i++) {
+        const int col = n0 + Ta::col(wave * C::AC + i, lane);
+        va[i] = (unsigned)pa[i] < (unsigned)g.P && col < g.N
+                    ? 2u * ((unsigned)pa[i] * (unsigned)g.N + (unsigned)col)
+                    : kNowhere;
+      }
+#pragma unroll
+      for (int i = 0; i < C::BC; i++) {
+        const int col = k0 + Tb::col(wave * C::BC + i, lane);
+        const int row = g.pair_rows ? pb[i] : pb[i] / g.k;
+        vb[i] = (unsigned)pb[i] < (unsigned)g.P && col < g.K
+                    ? 2u * ((unsigned)row * (unsigned)g.K + (unsigned)col)
+                    : kNowhere;
+      }
+      look(kb + 1);
     }
+    if (c < C::AC)
+      copy16(rsrc(g.dy, dbytes), va[c], 0, st + (wave * C::AC + c) * 1024);
+    else
+      copy16(rsrc(g.x, xbytes), vb[c - C::AC], 0,
+             st + C::B_AT + (wave * C::BC + c - C::AC) * 1024);
   };
   int offa[SM], offb[SN];
 #pragma unroll
@@ -546,35 +706,32 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradA
     for (int s = 0; s < SM; s++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[i][s][r] = 0.f;
-  k_loop<C>(lds, KB, copy, [&](const uint8_t* st, uint8_t* nx, int kb) {
-    const int next = kb + C::STAGES - 1;
-#pragma unroll
-    for (int s = 0; s < 4; s++) {
-      bf16x8 bf[SN], af[SM];
-#pragma unroll
-      for (int i = 0; i < SN; i++) bf[i] = Tb::frag(st + C::B_AT, offb[i], s);
-#pragma unroll
-      for (int j = 0; j < SM; j++) af[j] = Ta::frag(st, offa[j], s);
-#pragma unroll
-      for (int u = s * C::COPIES / 4; u < (s + 1) * C::COPIES / 4; u++) copy(nx, next, u);
-#pragma unroll
-      for (int j = 0; j < SM; j++)
-#pragma unroll
-        for (int i = 0; i < SN; i++)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[i], af[j], acc[i][j], 0, 0, 0);
-    }
-  });
-  constexpr int EB = F32 ? 4 : 2, RB = SN * 32 * EB;
-  static_assert(C::WAVES * 32 * RB <= (int)sizeof(lds), "every wave has room for 32 rows");
+  bf16x8 bf[2][SN], af[2][SM];
+  k_loop<C, SN + SM, SN * SM>(
+      lds, KB, copy,
+      [&](const uint8_t* st, int s, int r) {
+        if (r < SN)
+          bf[s & 1][r] = Tb::frag(st + C::B_AT, offb[r], s);
+        else
+          af[s & 1][r - SN] = Ta::frag(st, offa[r - SN], s);
+      },
+      [&](int s, int m) {
+        const int j = m / SN, i = m % SN;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(bf[s & 1][i], af[s & 1][j], acc[i][j],
+                                                            0, 0, 0);
+      });
+  constexpr int EB = F32 ? 4 : 2, ROW = SN * 32 * EB, RPI = 64 / (ROW / 16);
+  static_assert(C::WAVES * 32 * ROW <= (int)sizeof(lds), "every wave has room for 32 rows");
   __syncthreads();  // the last K block has been read
-  uint8_t* const mine = lds + wave * 32 * RB;
+  uint8_t* const mine = lds + wave * 32 * ROW;
   uint8_t* const out = reinterpret_cast<uint8_t*>(g.out) + (size_t)e * g.N * g.K * EB;
 #pragma unroll
   for (int s = 0; s < SM; s++)
-    turn_over<SN, F32>(
-        mine, [&](int i, int r) { return acc[i][s][r]; },
-        [&](int, int row, int byte, const uint8_t* v) {
-          const int n = n0 + (s * C::WM + wm) * 32 + row, k = k0 + wn * SN * 32 + byte / EB;
+    turn_over<4 * SN, F32, ROW>(
+        mine, [&](int q, int r) { return acc[q / 4][s][4 * (q % 4) + r]; },
+        [&](int u, int byte, const uint8_t* v) {
+          const int n = n0 + (s * C::WM + wm) * 32 + u * RPI + lane / (ROW / 16);
+          const int k = k0 + wn * SN * 32 + byte / EB;
           if (n >= g.N || k >= g.K) return;
           u32x4* o = reinterpret_cast<u32x4*>(out + ((size_t)n * g.K + k) * EB);
           u32x4 w = *reinterpret_cast<const u32x4*>(v);
@@ -584,13 +741,16 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradA
             for (int r = 0; r < 4; r++)
               w[r] = __float_as_uint(__uint_as_float(was[r]) + __uint_as_float(w[r]));
           }
-          *o = w;
+          // (past the L2, which holds the rows that the next tiles read)
+          __builtin_nontemporal_store(w, o);
         });
 }
 
 typedef Tile<256, 256, 2, 4, 2> Big;
-typedef Tile<128, 128, 2, 2, 2> Mid;
-typedef Tile<32, 256, 1, 4, 2> Low;
+typedef Tile<192, 256, 2, 4, 2> Wide;
+typedef Tile<128, 256, 2, 4, 2> Mid;
+typedef Tile<64, 128, 2, 2, 2> Half;
+typedef Tile<32, 128, 1, 2, 2> Low;
 
 template <class C, bool TRANS, int ACT, bool F32>
 hipError_t launch_tile(const GroupedArgs& g, hipStream_t s) {
@@ -600,8 +760,12 @@ hipError_t launch_tile(const GroupedArgs& g, hipStream_t s) {
   const long long ntm = g.M / C::BM + (g.E < g.P ? g.E : g.P);
   const long long total = (long long)((cols + TN - 1) / TN) * ntm;
   if (total > (1ll << 30)) return hipErrorInvalidValue;
+  // As many blocks as run at once, each with every so-many'th tile of its XCD (a K
+  // of one block has no second one to look the next tile up under: a block each).
+  const long long most = (long long)device_cu_count() * C::PER_CU;
+  const long long grid = g.K > 64 && total > most ? most : total;
   hipLaunchKernelGGL((grouped_tile_kernel<C, TRANS, ACT, F32>),
-                     dim3((unsigned)((total + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
+                     dim3((unsigned)((grid + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
   return hipGetLastError();
 }
 
@@ -615,21 +779,60 @@ hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The tile.  By the mean rows per expert, one that holds most experts' rows at once, so
+// that a matrix is read once, in us (128 experts, top-8; the row gradient's tiles with
+// SiLU * mul's gradient; "up" 1536 x 2048, "down" 2048 x 768):
+//   tokens (mean)     Low    Half   Mid    Wide   Big
+//   up    256 (16)    169    172    173    174    178
+//         512 (32)    212    171    174    177    176
+//         1024 (64)   240    223    184    182    186
+//         2048 (128)  359    307    272    209    204
+//         4000 (250)  626    481    375    340    308
+//   down  256 (16)     84     83     92     94     96
+//         1024 (64)   120    105     98    100    105
+//         2048 (128)  184    148    133    115    123
+//   back  256 (16)     84     94    111    114    122
+//         1024 (64)   141    137    128    131    144
+//         4000 (250)  349    291    265    252    302
+// Among the three widest the one whose rounds over the chip cost least, a round's cost
+// being its tile's rows + 128; where they leave half of the CUs without a tile, Half
+// (8 experts of 1536 x 2048, top-2, 1024 tokens: 32 against 39, 42 and 53 us).
+// Projections of few rows per expert go to the rows kernel ("up": 16 tokens (mean 1) 96
+// us, 128 (8) 168; Low 140 and 172).
 template <bool TRANS, int ACT, bool F32>
 hipError_t launch(const GroupedArgs& g, hipStream_t s) {
   const double mean = (double)g.P / g.E;
   if constexpr (!TRANS) {
-    if (mean <= 6) return launch_rows<ACT, F32>(g, s);
+    if (mean <= 8) return launch_rows<ACT, F32>(g, s);
   }
-  if (mean > 128) return launch_tile<Big, TRANS, ACT, F32>(g, s);
-  if (mean > 24) return launch_tile<Mid, TRANS, ACT, F32>(g, s);
-  return launch_tile<Low, TRANS, ACT, F32>(g, s);
+  if (mean <= 20) return launch_tile<Low, TRANS, ACT, F32>(g, s);
+  if (mean <= 44) return launch_tile<Half, TRANS, ACT, F32>(g, s);
+  const int cus = device_cu_count(), tn = ACT == kSilu ? 128 : 256;
+  const int cols = ACT == kSilu ? g.N / 2 : g.N, ntn = (cols + tn - 1) / tn;
+  auto tiles = [&](int bm) {  // expected, for a router that spreads the rows at random
+    const double of_one = g.E == 1 ? (g.P + bm - 1) / bm : mean / bm + 0.5;
+    return (of_one < 1 ? 1 : of_one) * g.E * ntn;
+  };
+  auto cost = [&](int bm) { return ceil(tiles(bm) / cus) * (bm + 128); };
+  if (tiles(128) < cus / 2) return launch_tile<Half, TRANS, ACT, F32>(g, s);
+  if (cost(256) <= cost(192) && cost(256) <= cost(128))
+    return launch_tile<Big, TRANS, ACT, F32>(g, s);
+  return cost(192) <= cost(128) ? launch_tile<Wide, TRANS, ACT, F32>(g, s)
+                                : launch_tile<Mid, TRANS, ACT, F32>(g, s);
 }
 
+// Weight gradients.  Short: three blocks on a CU, one storing while others add; Long:
+// the most values of K per byte copied.
+typedef Tile<128, 128, 2, 2, 2, 3, 2, 2> Short;
+typedef Tile<256, 256, 4, 4, 2, 4, 2> Long;
+
+template <class C>
+long long wgrad_tiles(const WgradArgs& g) {
+  return (long long)((g.K + C::BN - 1) / C::BN) * ((g.N + C::BM - 1) / C::BM) * g.E;
+}
 template <class C>
 hipError_t launch_wgrad(const WgradArgs& g, hipStream_t s) {
-  const long long total =
-      (long long)((g.K + C::BN - 1) / C::BN) * ((g.N + C::BM - 1) / C::BM) * g.E;
+  const long long total = wgrad_tiles<C>(g);
   if (total > (1ll << 30)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)((total + 7) / 8 * 8));
   if (g.out_f32)
@@ -655,7 +858,14 @@ hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t s) {
 }
 
 hipError_t launch_grouped_wgrad(const WgradArgs& g, hipStream_t s) {
-  return launch_wgrad<Mid>(g, s);
+  // Long where the experts have many rows and its rounds over the chip, each 1.12 of
+  // Short's, are the fewer (us, Short / Long: 128 experts of 1536 x 2048 in fp32, 128
+  // rows each 296 / 341, 250 rows 404 / 415; 8 experts, 1028 rows, 2048 x 1536 63 / 67;
+  // 1024 rows, 4096 x 4096 356 / 308; one, 4096 rows 163 / 134).
+  const double cus = device_cu_count(), shorts = wgrad_tiles<Short>(g) / (3 * cus);
+  if ((double)g.P / g.E > 320 && 1.12 * ceil(wgrad_tiles<Long>(g) / cus) < shorts)
+    return launch_wgrad<Long>(g, s);
+  return launch_wgrad<Short>(g, s);
 }
 
 }  // namespace qmoe

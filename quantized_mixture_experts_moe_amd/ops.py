@@ -34,8 +34,8 @@ EXPORTS = (
     "qmoe_decode", "qmoe_fp8_quant", "qmoe_fp8_matmul_workspace", "qmoe_fp8_matmul",
     "qmoe_fp8_grouped_matmul", "qmoe_balance_workspace", "qmoe_balance", "qmoe_balance_backward",
     "qmoe_pre_norm", "qmoe_post_norm", "qmoe_norm_backward_workspace", "qmoe_pre_norm_backward",
-    "qmoe_post_norm_backward", "qmoe_grouped_matmul", "qmoe_grouped_wgrad_workspace",
-    "qmoe_grouped_wgrad", "qmoe_combine_backward", "qmoe_w4_matmul_workspace", "qmoe_w4_matmul",
+    "qmoe_post_norm_backward", "qmoe_grouped_matmul", "qmoe_grouped_wgrad",
+    "qmoe_combine_backward", "qmoe_w4_matmul_workspace", "qmoe_w4_matmul",
 )
 # Forms in which pre_norm and post_norm write a norm (qmoe_form).
 NORM_FORMS = {"bf16": 0, "f32": 1, "int8": 2, "e4m3": 3, "e4m3_128": 4}
@@ -144,9 +144,8 @@ def _lib() -> ctypes.CDLL:
              [vp, vp, i32, vp, vp, i32, f32, f32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
             ("qmoe_grouped_matmul", ctypes.c_int,
              [vp, i32, vp, i32] + [vp] * 4 + [i32] * 7 + [vp, vp, i32, vp]),
-            ("qmoe_grouped_wgrad_workspace", sz, [i32] * 5),
             ("qmoe_grouped_wgrad", ctypes.c_int,
-             [vp, vp, i32, vp, vp] + [i32] * 6 + [vp, i32, i32, vp, sz, vp]),
+             [vp, vp, i32, vp, vp] + [i32] * 6 + [vp, i32, i32, vp]),
             ("qmoe_combine_backward", ctypes.c_int,
              [vp, vp, i32, vp, vp] + [i32] * 4 + [vp] * 5),
             ("qmoe_w4_matmul_workspace", sz, [i32] * 3),
@@ -767,7 +766,7 @@ def grouped_matmul(a: torch.Tensor, b: torch.Tensor, al: dict, k: int, pair_rows
 
 def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, al: dict, k: int, pair_rows: bool = False,
                   out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
-                  accumulate: bool = False, ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+                  accumulate: bool = False) -> torch.Tensor:
     """qmoe_grouped_wgrad: [E, N, K], dw[e] the sum over e's pairs p of
     dy[p]^T x[row(p)] (dy [T*k, N], x [T, K] or, with pair_rows, [T*k, K],
     bf16): the gradient of grouped_matmul's b for the gradient dy of its out.
@@ -781,15 +780,11 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, al: dict, k: int, pair_rows
     E, N, K = al["expert_offsets"].shape[0] - 1, dy.shape[1], x.shape[1]
     bm = _list(al, T, k, E)
     dev = _one_device(dy, x, al["sorted_pair_ids"], al["tile_expert"], al["expert_offsets"],
-                      al["num_padded"], ws, out)
+                      al["num_padded"], out)
     out = _out(out, (E, N, K), out_dtype, dev)
-    need = int(_lib().qmoe_grouped_wgrad_workspace(T, k, E, N, K))
-    if need and (ws is None or ws.numel() * ws.element_size() < need):
-        ws = _ws(need, dev)
     _call(dev, "qmoe_grouped_wgrad", _addr(dy), _addr(x), int(pair_rows),
           _addr(al["sorted_pair_ids"]), _addr(al["expert_offsets"]), T, k, E, bm, N, K, _addr(out),
-          _float_kind(out, "out"), int(accumulate), _addr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+          _float_kind(out, "out"), int(accumulate))
     return out
 
 

@@ -46,8 +46,7 @@ def test_grouped_matmul_refusals():
 
 def test_grouped_wgrad_refusals():
     c = _caller("qmoe_grouped_wgrad", dy=P, x=P, pair_rows=0, srt=P, off=P, T=4, k=2, E=8,
-                block_m=16, N=64, K=256, dw=P, out_dtype=1, accumulate=0, ws=P, ws_bytes=1 << 40,
-                stream=None)
+                block_m=16, N=64, K=256, dw=P, out_dtype=1, accumulate=0, stream=None)
     for bad in (dict(pair_rows=2), dict(T=-1), dict(k=0), dict(k=9), dict(E=0), dict(block_m=8),
                 dict(T=1 << 30), dict(N=0), dict(K=0), dict(out_dtype=2), dict(accumulate=2),
                 dict(accumulate=1, out_dtype=0), dict(dy=None), dict(x=None), dict(srt=None),
@@ -56,17 +55,6 @@ def test_grouped_wgrad_refusals():
     for big in (dict(E=1025), dict(N=60), dict(K=260), dict(N=(1 << 22) + 8), dict(K=(1 << 22) + 8),
                 dict(T=1 << 20, K=2048), dict(T=1 << 19, N=2048)):
         assert c(**big) == UNS, big
-    ws = ops.lib().qmoe_grouped_wgrad_workspace
-    for bad in ((-1, 2, 8, 64, 64), (4, 0, 8, 64, 64), (4, 2, 0, 64, 64), (4, 2, 8, 0, 64),
-                (4, 2, 8, 64, 0)):
-        assert ws(*bad) == 0
-    for T, k, E, N, K in ((8192, 2, 8, 256, 256), (4096, 1, 1, 64, 64), (64, 2, 8, 256, 128)):
-        need = ws(T, k, E, N, K)
-        assert need % 256 == 0
-        if need:
-            at = dict(T=T, k=k, E=E, N=N, K=K)
-            assert c(**at, ws_bytes=need - 1) == INV and c(**at, ws=None) == INV
-            assert c(**at, ws=ODD) == INV
 
 
 def test_combine_backward_refusals():
