@@ -99,7 +99,8 @@ struct W4Args {
   bool act, out_f32;
   const void* add;       // [M, columns of out] or nullptr
   void* out;             // [M, N]; act [M, N / 2]
-  float* parts;          // sums of a K split
+  float* parts;          // sums of a K split [splits, M, N]
+  int splits, split_kb;  // parts, K blocks of 128 per part (set by the launcher)
 };
 size_t w4_matmul_parts_bytes(int M, int N, int K);
 hipError_t launch_w4_matmul(const W4Args& g, hipStream_t s);

@@ -13,6 +13,48 @@ namespace {
 using namespace bk;
 constexpr int kGroup = 8, kMaxK = 16;
 
+// Eight values as loaded, read once (past the caches that hold dout); and stores that
+// no other wave reads.
+template <bool F32>
+struct Raw8 {
+  u32x4 q[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ inline Raw8<F32> load_once(const void* p, size_t i) {
+  Raw8<F32> r;
+  const u32x4* q = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(p) +
+                                                  i * (F32 ? 4 : 2));
+  r.q[0] = __builtin_nontemporal_load(q);
+  if constexpr (F32) r.q[1] = __builtin_nontemporal_load(q + 1);
+  return r;
+}
+template <bool F32>
+__device__ inline void unpack(const Raw8<F32>& r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    if constexpr (F32)
+      v[i] = __uint_as_float(r.q[i / 4][i % 4]);
+    else
+      v[i] = __uint_as_float(i & 1 ? r.q[0][i / 2] & 0xffff0000u : r.q[0][i / 2] << 16);
+  }
+}
+template <bool F32>
+__device__ inline void store_past(void* p, size_t i, const float v[8]) {
+  u32x4* q = reinterpret_cast<u32x4*>(reinterpret_cast<uint8_t*>(p) + i * (F32 ? 4 : 2));
+  if constexpr (F32) {
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+      __builtin_nontemporal_store(
+          u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])},
+          q + h);
+  } else {
+    __builtin_nontemporal_store(u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                      pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])},
+                                q);
+  }
+}
+
 template <int WPT, bool F32>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g) {
   constexpr int TPB = 4 / WPT;  // tokens per block
@@ -31,36 +73,35 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g)
 #pragma unroll
       for (int u = 0; u < kGroup; u++) {
         dot[u] = 0.f;
-        in[u] = false;
-        w[u] = 0.f;
-        if (j0 + u < k) {
-          in[u] = (unsigned)g.ids[p0 + j0 + u] < (unsigned)g.E;
-          w[u] = g.w[p0 + j0 + u];
-        }
+        const int j = min(j0 + u, k - 1);
+        in[u] = j0 + u < k && (unsigned)g.ids[p0 + j] < (unsigned)g.E;
+        w[u] = g.w[p0 + j];
       }
       for (int c = c0; c < H; c += step) {
         float d[8];
+        Raw8<F32> y[kGroup];  // (all loads before the first is used)
         load8<F32>(g.dout, (size_t)t * H + c, d);
-        float y[kGroup][8];
 #pragma unroll
         for (int u = 0; u < kGroup; u++)
-          if (in[u]) load8<F32>(g.y, (p0 + j0 + u) * H + c, y[u]);
+          if (j0 + u < k) y[u] = load_once<F32>(g.y, (p0 + j0 + u) * H + c);
 #pragma unroll
         for (int u = 0; u < kGroup; u++) {
-          if (j0 + u >= k) break;
+          if (j0 + u >= k) continue;
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; i++) v[i] = in[u] ? w[u] * d[i] : 0.f;
-          store8<F32>(g.dy, (p0 + j0 + u) * H + c, v);
           if (in[u]) {
+            float f[8];
+            unpack<F32>(y[u], f);
 #pragma unroll
-            for (int i = 0; i < 8; i++) dot[u] = __builtin_fmaf(d[i], y[u][i], dot[u]);
+            for (int i = 0; i < 8; i++) dot[u] = __builtin_fmaf(d[i], f[i], dot[u]);
           }
+          store_past<F32>(g.dy, (p0 + j0 + u) * H + c, v);
         }
       }
 #pragma unroll
       for (int u = 0; u < kGroup; u++) {
-        if (j0 + u >= k) break;
+        if (j0 + u >= k) continue;
         const float s = wave_sum(dot[u]);
         if (lane == 0) sums[wave][j0 + u] = s;
       }
