@@ -511,96 +511,109 @@ __global__ __launch_bounds__(C::THREADS, 2) void w4_tile_kernel(W4Args g) {
     for (int c = 0; c < C::XC + C::CC; c++) copy(nx, kb + 1, c);
     // Blocks per group that are summed before the scale (64 values: two have one scale).
     constexpr int BPG = FMT == kInt4G128 ? 4 : 1;
-    bf16x8 x[SM][2], w[SN][2];
+    constexpr int AHEAD = BPG == 1 ? 2 : 1;  // blocks in registers
+    bf16x8 x[AHEAD][SM][2], w[AHEAD][SN][2];
+    u32x2 c[SN];
     auto read = [&](int b) {
 #pragma unroll
       for (int j = 0; j < SM; j++)
 #pragma unroll
         for (int s = 0; s < 2; s++)
-          x[j][s] = __builtin_bit_cast(
+          x[b % AHEAD][j][s] = __builtin_bit_cast(
               bf16x8, *reinterpret_cast<const u32x4*>(st + (b / 2) * C::BM * 128 +
                                                       (j * C::WM + wm) * 4096 + off[b & 1][s]));
 #pragma unroll
-      for (int i = 0; i < SN; i++) {
-        const u32x2 c = *reinterpret_cast<const u32x2*>(
+      for (int i = 0; i < SN; i++)
+        c[i] = *reinterpret_cast<const u32x2*>(
             st + C::C_AT + ((wn * SN + i) * 32 + r32) * 64 + 16 * (b ^ ((r32 >> 2) & 3)) + 8 * h);
-        w[i][0] = widen8<FMT>(c[0]);
-        w[i][1] = widen8<FMT>(c[1]);
-      }
     };
-    // -1.5 sum x of the block, on top of t.
-    auto offset = [&](int j, f32x16 t) {
-      if constexpr (FMT != kMxfp4) {
+    auto widen = [&](int b) {
 #pragma unroll
-        for (int s = 0; s < 2; s++)
-          t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][s], minus, t, 0, 0, 0);
-      }
-      return t;
-    };
-    auto product = [&](int j, int i, f32x16 t) {
+      for (int i = 0; i < SN; i++)
 #pragma unroll
-      for (int s = 0; s < 2; s++)
-        t = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[j][s], w[i][s], t, 0, 0, 0);
-      return t;
+        for (int s = 0; s < 2; s++) w[b % AHEAD][i][s] = widen8<FMT>(c[i][s]);
     };
     f32x16 zero;
 #pragma unroll
     for (int r = 0; r < 16; r++) zero[r] = 0.f;
+    read(0);
+    widen(0);
     if constexpr (BPG == 1) {
-      // A row of sub-tiles' scaling runs behind the next row's products.
+      // Row q % SM of sub-tiles in block q / SM.  Between its matrix instructions run
+      // the scaling of the row before and the widening of the next block's codes, which
+      // are as long.
+      f32x16 t[2][SN];
+      float f[2][SN];
+      auto scaled = [&](int q) {
 #pragma unroll
-      for (int b = 0; b < 4; b++) {
-        read(b);
-        float s[SN];
+        for (int i = 0; i < SN; i++)
 #pragma unroll
-        for (int i = 0; i < SN; i++) s[i] = scale_of<FMT>(sc[i], b);
-        f32x16 t[2][SN];
-        auto scaled = [&](int j) {
+          for (int r = 0; r < 16; r++)
+            acc[q % SM][i][r] =
+                __builtin_fmaf(t[q & 1][i][r], f[q / SM & 1][i], acc[q % SM][i][r]);
+      };
+#pragma unroll
+      for (int q = 0; q < 4 * SM; q++) {
+        const int b = q / SM, j = q % SM;
+        if (j == 0) {
+#pragma unroll
+          for (int i = 0; i < SN; i++) f[b & 1][i] = scale_of<FMT>(sc[i], b);
+          if (b < 3) read(b + 1);
+        }
+        f32x16 z = zero;
+        if constexpr (FMT != kMxfp4) {
+#pragma unroll
+          for (int s = 0; s < 2; s++)
+            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[b % AHEAD][j][s], minus, z, 0, 0, 0);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; s++)
 #pragma unroll
           for (int i = 0; i < SN; i++)
+            t[q & 1][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                x[b % AHEAD][j][s], w[b % AHEAD][i][s], s == 0 ? z : t[q & 1][i], 0, 0, 0);
+        if (q > 0) scaled(q - 1);
+        if (j == SM - 1 && b < 3) widen(b + 1);
+        constexpr int PRODUCTS = 2 * SN + (FMT == kMxfp4 ? 0 : 2);
 #pragma unroll
-            for (int r = 0; r < 16; r++)
-              acc[j][i][r] = __builtin_fmaf(t[j & 1][i][r], s[i], acc[j][i][r]);
-        };
-#pragma unroll
-        for (int j = 0; j < SM; j++) {
-          const f32x16 z = offset(j, zero);
-#pragma unroll
-          for (int h2 = 0; h2 < 2; h2++)
-#pragma unroll
-            for (int i = 0; i < SN; i++)
-              t[j & 1][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  x[j][h2], w[i][h2], h2 == 0 ? z : t[j & 1][i], 0, 0, 0);
-          if (j > 0) scaled(j - 1);
+        for (int m = 0; m < PRODUCTS; m++) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+          __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);  // vector instructions
         }
-        scaled(SM - 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      scaled(4 * SM - 1);
     } else {
+      f32x16 t[SM][SN], z[SM];
 #pragma unroll
-      for (int b0 = 0; b0 < 4; b0 += BPG) {
-        f32x16 t[SM][SN], z[SM];
-#pragma unroll
-        for (int b = b0; b < b0 + BPG; b++) {
+      for (int b = 0; b < 4; b++) {
+        if (b > 0) {
           read(b);
-#pragma unroll
-          for (int j = 0; j < SM; j++) {
-            z[j] = offset(j, b == b0 ? zero : z[j]);
-#pragma unroll
-            for (int i = 0; i < SN; i++) t[j][i] = product(j, i, b == b0 ? zero : t[j][i]);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+          widen(b);
         }
 #pragma unroll
-        for (int j = 0; j < SM; j++)
+        for (int j = 0; j < SM; j++) {
+          if (b == 0) z[j] = zero;
 #pragma unroll
-          for (int i = 0; i < SN; i++) {
-            const float s = scale_of<FMT>(sc[i], b0);
+          for (int s = 0; s < 2; s++) {
+            z[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[b % AHEAD][j][s], minus, z[j], 0, 0, 0);
 #pragma unroll
-            for (int r = 0; r < 16; r++)
-              acc[j][i][r] = __builtin_fmaf(t[j][i][r] + z[j][r], s, acc[j][i][r]);
+            for (int i = 0; i < SN; i++)
+              t[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  x[b % AHEAD][j][s], w[b % AHEAD][i][s], b == 0 && s == 0 ? zero : t[j][i], 0, 0, 0);
           }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int j = 0; j < SM; j++)
+#pragma unroll
+        for (int i = 0; i < SN; i++) {
+          const float s = scale_of<FMT>(sc[i], 0);
+#pragma unroll
+          for (int r = 0; r < 16; r++)
+            acc[j][i][r] = __builtin_fmaf(t[j][i][r] + z[j][r], s, acc[j][i][r]);
+        }
     }
   };
   RawScale sc[SN], next[SN];

@@ -7,6 +7,7 @@ kernels.  Loading fails loudly when the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -798,18 +799,20 @@ def combine_backward(dout: torch.Tensor, y_pairs: torch.Tensor, topk_ids: torch.
     T, H = dout.shape
     k = topk_w.shape[1]
     dt = _float_kind(dout, "dout")
-    _tensor(y_pairs, "y_pairs", (T * k, H), dout.dtype)
-    _tensor(topk_w, "topk_w", (T, k), torch.float32)
-    _tensor(topk_ids, "topk_ids", (T, k), torch.int32)
+    if (y_pairs.shape != (T * k, H) or y_pairs.dtype != dout.dtype or topk_w.shape[0] != T
+            or topk_ids.shape != (T, k) or topk_w.dtype != torch.float32
+            or topk_ids.dtype != torch.int32):
+        _tensor(y_pairs, "y_pairs", (T * k, H), dout.dtype)
+        _tensor(topk_w, "topk_w", (T, k), torch.float32)
+        _tensor(topk_ids, "topk_ids", (T, k), torch.int32)
     if add is not None:
         _tensor(add, "add", (T, E), torch.float32)
     dev = _one_device(dout, y_pairs, topk_ids, topk_w, add)
-    r = {"dy": torch.empty_like(y_pairs), "dw": torch.empty_like(topk_w),
-         "dlogits": torch.empty((T, E), dtype=torch.float32, device=dev)}
-    _call(dev, "qmoe_combine_backward", _addr(dout), _addr(y_pairs), dt, _addr(topk_ids),
-          _addr(topk_w), T, k, H, E, _addr(add), r["dy"].data_ptr(), r["dw"].data_ptr(),
-          r["dlogits"].data_ptr())
-    return r
+    args = _addr(dout), _addr(y_pairs), dt, _addr(topk_ids), _addr(topk_w), T, k, H, E, _addr(add)
+    dy, dw = torch.empty_like(y_pairs), torch.empty_like(topk_w)
+    dz = torch.empty((T, E), dtype=torch.float32, device=dev)
+    _call(dev, "qmoe_combine_backward", *args, dy.data_ptr(), dw.data_ptr(), dz.data_ptr())
+    return {"dy": dy, "dw": dw, "dlogits": dz}
 
 
 def bf16_moe_forward(logits: torch.Tensor, x: torch.Tensor, weights: dict, k: int) -> dict:
@@ -853,6 +856,12 @@ def w4_matmul_workspace(M: int, N: int, K: int) -> int:
     return int(_lib().qmoe_w4_matmul_workspace(M, N, K))
 
 
+# (A rule on the sizes: one look-up per shape and process.)
+_w4_workspace = functools.lru_cache(maxsize=1024)(w4_matmul_workspace)
+# Scale types of 4-bit weights: the format, and how many values a scale may be for.
+_W4_SCALES = {torch.float16: (W4_INT4, (32, 64, 128)), torch.uint8: (W4_MXFP4, (32,))}
+
+
 def w4_matmul(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
               act: Optional[str] = None, add: Optional[torch.Tensor] = None,
               out_dtype: torch.dtype = torch.bfloat16, ws: Optional[torch.Tensor] = None,
@@ -862,32 +871,36 @@ def w4_matmul(x: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
     or 128; or uint8 (e8m0) [N, K/32], e2m1 codes.  act="silu_mul": the weights
     are gate | up rows, the result SiLU(g) * u [M, N/2].  add: a tensor of the
     result's shape and type, added before the rounding (it may be ``out``)."""
-    _need(act in (None, "silu_mul"), "act must be None or 'silu_mul', not %r", act)
+    if act is not None and act != "silu_mul":
+        raise ValueError(f"act must be None or 'silu_mul', not {act!r}")
     _need(x.dim() == 2 and codes.dim() == 2 and scale.dim() == 2,
           "x, codes and scale must have 2 axes")
     M, K = x.shape
-    N, groups = codes.shape[0], scale.shape[1]
-    _tensor(x, "x", (M, K), torch.bfloat16)
-    _tensor(codes, "codes", (N, K // 2), torch.uint8)
-    _tensor(scale, "scale", (N, groups), torch.float16, torch.uint8)
-    fmt = W4_INT4 if scale.dtype == torch.float16 else W4_MXFP4
-    _need(groups > 0 and K % groups == 0, "%d scales do not divide %d values", groups, K)
-    group = K // groups
-    _need(group in ((32, 64, 128) if fmt == W4_INT4 else (32,)),
-          "groups of %d values are not supported", group)
-    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
-    _need(act is None or N % 2 == 0, "act='silu_mul' takes an even number of weight rows")
-    cols = N // 2 if act else N
+    N, groups = scale.shape
+    if (codes.shape != (N, K // 2) or x.dtype != torch.bfloat16 or codes.dtype != torch.uint8
+            or scale.dtype not in _W4_SCALES):
+        _tensor(x, "x", (M, K), torch.bfloat16)
+        _tensor(codes, "codes", (N, K // 2), torch.uint8)
+        _tensor(scale, "scale", (N, groups), *_W4_SCALES)
+    fmt, groups_of = _W4_SCALES[scale.dtype]
+    if groups == 0 or K % groups or K // groups not in groups_of:
+        raise ValueError(f"{groups} scales for {K} values: groups of {groups_of} are supported")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("out_dtype must be bfloat16 or float32")
+    cols = N
+    if act:
+        _need(N % 2 == 0, "act='silu_mul' takes an even number of weight rows")
+        cols = N // 2
     if add is not None:
         _tensor(add, "add", (M, cols), out_dtype)
     dev = _one_device(x, codes, scale, add, ws, out)
     out = _out(out, (M, cols), out_dtype, dev)
-    need = w4_matmul_workspace(M, N, K)
+    need = _w4_workspace(M, N, K)
     if need and (ws is None or ws.numel() * ws.element_size() < need):
         ws = _ws(need, dev)
-    _call(dev, "qmoe_w4_matmul", _addr(x), _addr(codes), _addr(scale), fmt, group, M, N, K,
-          ACTS[act], _addr(add), _addr(out), _float_kind(out, "out"), _addr(ws),
-          0 if ws is None else ws.numel() * ws.element_size())
+    _call(dev, "qmoe_w4_matmul", _addr(x), _addr(codes), _addr(scale), fmt, K // groups, M, N, K,
+          ACTS[act], _addr(add), _addr(out), _float_kind(out, "out"), _addr(ws) if need else None,
+          ws.numel() * ws.element_size() if need else 0)
     return out
 
 
