@@ -347,8 +347,9 @@ qmoe_status qmoe_decode(const qmoe_ffn_desc* d, const float* logits, const void*
  * with a scale for each block of 128 (dense, and for the experts of a
  * routed batch) with the quantizer that feeds them, the experts' products in
  * bf16 with their gradients and the routed sum's, dense products with 4-bit
- * weights, the router's balance loss, and the norms before and after a block.  The conventions at the top
- * of this file hold for them.  Arrays are contiguous.                    */
+ * weights, the router's balance loss, and the norms before and after a
+ * block.  The conventions at the top of this file hold for them.  Arrays are
+ * contiguous.                                                            */
 
 /* ---------------------------------------------------------------------
  * qmoe_fp8_quant -- x to OCP e4m3 codes with one fp32 scale per group:

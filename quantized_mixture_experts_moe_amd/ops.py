@@ -702,16 +702,26 @@ ACTS = {None: 0, "silu_mul": 1, "silu_mul_backward": 2}
 W4_INT4, W4_MXFP4 = 0, 1
 
 
+# (A formula of the sizes: one look-up per process and set of them.)
+_capacity = functools.lru_cache(maxsize=4096)(align_capacity)
+_I32, _BF16 = torch.int32, torch.bfloat16
+
+
 def _list(al: dict, T: int, k: int, E: int):
-    """Checks align's (or route_align's) result for these sizes; returns block_m."""
-    bm = al["block_m"]
-    cap = align_capacity(T, k, E, bm)
+    """Checks align's (or route_align's) result for these sizes; returns (block_m,
+    sorted_pair_ids, tile_expert, expert_offsets, num_padded)."""
+    bm, order, tiles = al["block_m"], al["sorted_pair_ids"], al["tile_expert"]
+    offsets, padded = al["expert_offsets"], al["num_padded"]
+    cap = _capacity(T, k, E, bm)
     _need(cap > 0 or T == 0, "bad sizes: T %d, k %d, E %d, block_m %d", T, k, E, bm)
-    _tensor(al["sorted_pair_ids"], "sorted_pair_ids", (cap,), torch.int32)
-    _tensor(al["tile_expert"], "tile_expert", (cap // bm,), torch.int32)
-    _tensor(al["expert_offsets"], "expert_offsets", (E + 1,), torch.int32)
-    _tensor(al["num_padded"], "num_padded", (1,), torch.int32)
-    return bm
+    if (order.shape != (cap,) or tiles.shape != (cap // bm,) or offsets.shape != (E + 1,)
+            or padded.shape != (1,) or order.dtype != _I32 or tiles.dtype != _I32
+            or offsets.dtype != _I32 or padded.dtype != _I32):
+        _tensor(order, "sorted_pair_ids", (cap,), _I32)
+        _tensor(tiles, "tile_expert", (cap // bm,), _I32)
+        _tensor(offsets, "expert_offsets", (E + 1,), _I32)
+        _tensor(padded, "num_padded", (1,), _I32)
+    return bm, order, tiles, offsets, padded
 
 
 def _rows_of(x, name: str, k: int, pair_rows: bool) -> int:
@@ -735,33 +745,35 @@ def grouped_matmul(a: torch.Tensor, b: torch.Tensor, al: dict, k: int, pair_rows
     tensor [T*k, N], receives g | u.  act="silu_mul_backward" (with trans):
     the gradient of g | u [T*k, 2N] for the gradient a . b of SiLU(g) * u,
     gu being what the forward call kept."""
-    _need(act in ACTS, "act must be one of %s, not %r", list(ACTS), act)
+    code = ACTS.get(act, -1)
+    if code < 0:
+        raise ValueError(f"act must be one of {list(ACTS)}, not {act!r}")
     _need(b.dim() == 3, "b must be [E, N, K]")
-    E = b.shape[0]
-    N, K = (b.shape[2], b.shape[1]) if trans else (b.shape[1], b.shape[2])
+    E, N, K = b.shape
+    if trans:
+        N, K = K, N
     T = _rows_of(a, "a", k, pair_rows)
     _need(a.shape[1] == K, "a's rows have %d values, b's %d", a.shape[1], K)
-    _need(b.dtype == torch.bfloat16, "b must be bfloat16, not %s", b.dtype)
-    _need(out_dtype in (torch.bfloat16, torch.float32), "out_dtype must be bfloat16 or float32")
-    if act == "silu_mul":
-        _need(not trans and N % 2 == 0, "act='silu_mul' takes b [E, 2I, K] without trans")
-        cols, gcols = N // 2, N
-    elif act == "silu_mul_backward":
-        _need(trans and gu is not None, "act='silu_mul_backward' goes with trans and takes gu")
-        cols, gcols = 2 * N, 2 * N
-    else:
+    _need(b.dtype == _BF16, "b must be bfloat16, not %s", b.dtype)
+    _need(out_dtype == _BF16 or out_dtype == torch.float32,
+          "out_dtype must be bfloat16 or float32")
+    cols = N
+    if code == 0:
         _need(gu is None, "gu goes with an act")
-        cols, gcols = N, 0
+    elif code == 1:
+        _need(not trans and N % 2 == 0, "act='silu_mul' takes b [E, 2I, K] without trans")
+        cols = N // 2
+    else:
+        _need(trans and gu is not None, "act='silu_mul_backward' goes with trans and takes gu")
+        cols = 2 * N
     if gu is not None:
-        _tensor(gu, "gu", (T * k, gcols), torch.bfloat16)
-    bm = _list(al, T, k, E)
-    dev = _one_device(a, b, al["sorted_pair_ids"], al["tile_expert"], al["expert_offsets"],
-                      al["num_padded"], gu, out)
+        _tensor(gu, "gu", (T * k, N if code == 1 else 2 * N), _BF16)
+    bm, order, tiles, offsets, padded = _list(al, T, k, E)
+    dev = _one_device(a, b, order, tiles, offsets, padded, gu, out)
     out = _out(out, (T * k, cols), out_dtype, dev)
-    _call(dev, "qmoe_grouped_matmul", _addr(a), int(pair_rows), _addr(b), int(trans),
-          _addr(al["sorted_pair_ids"]), _addr(al["tile_expert"]), _addr(al["expert_offsets"]),
-          _addr(al["num_padded"]), T, k, E, bm, N, K, ACTS[act], _addr(gu), _addr(out),
-          _float_kind(out, "out"))
+    _call(dev, "qmoe_grouped_matmul", _addr(a), pair_rows, _addr(b), trans, _addr(order),
+          _addr(tiles), _addr(offsets), _addr(padded), T, k, E, bm, N, K, code, _addr(gu),
+          _addr(out), _float_kind(out, "out"))
     return out
 
 
@@ -779,13 +791,11 @@ def grouped_wgrad(dy: torch.Tensor, x: torch.Tensor, al: dict, k: int, pair_rows
     _need(not accumulate or (out is not None and out_dtype == torch.float32),
           "accumulate takes an fp32 out")
     E, N, K = al["expert_offsets"].shape[0] - 1, dy.shape[1], x.shape[1]
-    bm = _list(al, T, k, E)
-    dev = _one_device(dy, x, al["sorted_pair_ids"], al["tile_expert"], al["expert_offsets"],
-                      al["num_padded"], out)
+    bm, order, tiles, offsets, padded = _list(al, T, k, E)
+    dev = _one_device(dy, x, order, tiles, offsets, padded, out)
     out = _out(out, (E, N, K), out_dtype, dev)
-    _call(dev, "qmoe_grouped_wgrad", _addr(dy), _addr(x), int(pair_rows),
-          _addr(al["sorted_pair_ids"]), _addr(al["expert_offsets"]), T, k, E, bm, N, K, _addr(out),
-          _float_kind(out, "out"), int(accumulate))
+    _call(dev, "qmoe_grouped_wgrad", _addr(dy), _addr(x), pair_rows, _addr(order), _addr(offsets),
+          T, k, E, bm, N, K, _addr(out), _float_kind(out, "out"), accumulate)
     return out
 
 

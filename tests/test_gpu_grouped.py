@@ -73,7 +73,7 @@ SIZES = [(1, 8, 2, 64, 64), (1, 1, 1, 8, 8), (3, 16, 4, 96, 136), (7, 4, 4, 48, 
 def test_matmul(T, E, k, N, K, trans):
     print(f"grouped_matmul {T} {E} {k} {N} {K} trans {trans}", flush=True)
     ids = _ids(T, E, k, T + E, skew=T % 2 == 0)
-    b = _rand(E, K, N, seed=1, scale=K ** -0.5) if trans else _rand(E, N, K, seed=1, scale=K ** -0.5)
+    b = _rand(E, *((K, N) if trans else (N, K)), seed=1, scale=K ** -0.5)
     for pair_rows in (False, True):
         a = _rand(T * k if pair_rows else T, K, seed=2)
         ref, mag = _plain(a, b, ids, pair_rows, trans)
@@ -104,7 +104,8 @@ def test_silu_mul(T, E, k, N, K):
     eg, eu = (_sum_tol(K) * 1.01 * mag).chunk(2, 1)
     ref = g * torch.sigmoid(g) * u
     # SiLU's slope is below 1.1; its evaluation and the products are within 8 half steps
-    err = 1.1 * u.abs() * eg + (g * torch.sigmoid(g)).abs() * eu + 1.1 * eg * eu + 8 * R.U32 * ref.abs()
+    err = (1.1 * u.abs() * eg + (g * torch.sigmoid(g)).abs() * eu + 1.1 * eg * eu
+           + 8 * R.U32 * ref.abs())
     for dt in (BF, F32):
         gu = torch.full((T * k, N), float("nan"), dtype=BF, device="cuda")
         h = ops.grouped_matmul(a, b, al, k, act="silu_mul", gu=gu, out_dtype=dt)
@@ -233,7 +234,8 @@ def test_what_is_not_finite_stays_in_its_row(T):
 
 # ---------------------------------------------------------------- the routed sum's gradient
 
-@pytest.mark.parametrize("T,E,k,H", [(1, 4, 1, 8), (5, 8, 2, 256), (64, 8, 8, 512), (33, 60, 4, 520),
+@pytest.mark.parametrize("T,E,k,H", [(1, 4, 1, 8), (5, 8, 2, 256), (64, 8, 8, 512),
+                                     (33, 60, 4, 520),
                                      (257, 512, 10, 2048), (3, 1024, 16, 4096), (130, 17, 5, 1000)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_combine_backward(T, E, k, H, dt):
@@ -295,7 +297,7 @@ def test_combine_backward_bad_ids_and_in_place():
     r2 = ops.combine_backward(dout, y, ids, w, E, add=add)
     lib, s = ops.lib(), torch.cuda.current_stream().cuda_stream
     dz, dy = add.clone(), y.clone()
-    assert lib.qmoe_combine_backward(dout.data_ptr(), dy.data_ptr(), 0, ids.data_ptr(), w.data_ptr(),
-                                     T, k, H, E, dz.data_ptr(), dy.data_ptr(), None, dz.data_ptr(),
-                                     s) == 0
+    assert lib.qmoe_combine_backward(dout.data_ptr(), dy.data_ptr(), 0, ids.data_ptr(),
+                                     w.data_ptr(), T, k, H, E, dz.data_ptr(), dy.data_ptr(), None,
+                                     dz.data_ptr(), s) == 0
     assert torch.equal(dz, r2["dlogits"]) and torch.equal(dy, r2["dy"])

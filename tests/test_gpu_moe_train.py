@@ -33,7 +33,8 @@ def _plain(logits, x, w13, w2, ids):
         p = (flat == e).nonzero().reshape(-1)
         if p.numel():
             g, u = (x[p // k] @ w13[e].t()).chunk(2, 1)
-            out = out.index_add(0, p // k, w[p].unsqueeze(1) * ((g * torch.sigmoid(g) * u) @ w2[e].t()))
+            y = (g * torch.sigmoid(g) * u) @ w2[e].t()
+            out = out.index_add(0, p // k, w[p].unsqueeze(1) * y)
     return out
 
 

@@ -57,7 +57,8 @@ def _check(got, ref, tol, what=None):
 
 
 FORMATS = [(32, False), (64, False), (128, False), (32, True)]
-# M, N, K in units of the group: tails of the K step, odd columns, both sides of every choice of kernel
+# M, N, K in units of the group: tails of the K step, odd columns, both sides of every
+# choice of kernel
 SIZES = [(1, 1, 1), (1, 40, 3), (2, 1000, 33), (5, 17, 8), (16, 333, 5), (17, 64, 12), (33, 130, 7),
          (64, 48, 4), (65, 257, 9), (130, 512, 6), (300, 129, 10), (1, 4096, 32), (257, 1024, 16),
          (2, 12300, 2), (8, 7000, 3), (9, 10300, 3), (50, 7000, 9), (130, 16400, 4), (100, 512, 64)]
@@ -85,7 +86,8 @@ def test_w4_matmul(M, N, kg, group, mx):
 
 @pytest.mark.parametrize("group,mx", FORMATS)
 @pytest.mark.parametrize("M,N,kg", [(1, 2, 1), (1, 768, 16), (5, 90, 9), (16, 1024, 5), (40, 34, 8),
-                                    (130, 386, 7), (300, 512, 4), (100, 512, 64), (12, 14000, 5), (200, 33000, 2)])
+                                    (130, 386, 7), (300, 512, 4), (100, 512, 64),
+                                    (12, 14000, 5), (200, 33000, 2)])
 def test_w4_silu_mul(M, N, kg, group, mx):
     K = kg * group
     print(f"w4 silu_mul {M} {N} {K} group {group} mxfp4 {mx}", flush=True)

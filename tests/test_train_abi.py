@@ -37,9 +37,10 @@ def test_grouped_matmul_refusals():
                 dict(off=None), dict(npad=None), dict(out=None), dict(a=ODD), dict(b=ODD),
                 dict(out=ODD), dict(act=1, gu=ODD)):
         assert c(**bad) == INV, bad
-    for big in (dict(E=1025, k=2), dict(N=60), dict(K=260), dict(act=1, N=72), dict(N=(1 << 22) + 8),
-                dict(K=(1 << 22) + 8), dict(N=1 << 20, K=2048), dict(T=1 << 20, K=2048),
-                dict(T=1 << 19, K=2048, pair_rows=1), dict(trans=1, N=1 << 20, K=2048)):
+    for big in (dict(E=1025, k=2), dict(N=60), dict(K=260), dict(act=1, N=72),
+                dict(N=(1 << 22) + 8), dict(K=(1 << 22) + 8), dict(N=1 << 20, K=2048),
+                dict(T=1 << 20, K=2048), dict(T=1 << 19, K=2048, pair_rows=1),
+                dict(trans=1, N=1 << 20, K=2048)):
         assert c(**big) == UNS, big
     assert c(T=0, a=None) == OK
 
@@ -77,7 +78,8 @@ def test_w4_matmul_refusals():
                 dict(K=192, group=128), dict(act=2), dict(act=1, N=63), dict(out_dtype=3),
                 dict(x=None), dict(codes=None), dict(scale=None), dict(out=None), dict(x=ODD),
                 dict(codes=ODD), dict(scale=ODD), dict(out=ctypes.c_void_p(0x10001)),
-                dict(add=ctypes.c_void_p(0x10001)), dict(out_dtype=1, out=ctypes.c_void_p(0x10002))):
+                dict(add=ctypes.c_void_p(0x10001)),
+                dict(out_dtype=1, out=ctypes.c_void_p(0x10002))):
         assert c(**bad) == INV, bad
     for big in (dict(M=(1 << 24) + 1), dict(N=(1 << 24) + 1), dict(K=1 << 23)):
         assert c(**big) == UNS, big
