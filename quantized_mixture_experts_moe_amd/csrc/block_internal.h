@@ -63,6 +63,7 @@ struct GroupedArgs {
   const int32_t* num_padded;
   int P, k, block_m, E;
   bool pair_rows;
+  int slots;  // blocks that run at once (set at the launch)
 };
 struct WgradArgs {
   const uint16_t* dy;  // [P, N]

@@ -12,7 +12,7 @@
 // 6.9 TB/s, of a large dense bf16 product 1.45 PFLOP/s): 4 tokens on 128 experts of
 // 1536 x 2048 (top-8) 38 us, 183 MB of weights at 4.8 TB/s; 2048 tokens there with
 // SiLU * mul and the gate/up kept 197-214 us, 0.89 GB at 4.2-4.5 TB/s; their way back
-// through the down projection 155 us, 0.57 GB at 3.7 TB/s; 4111 tokens on 8 experts of
+// through the down projection 127-134 us, 0.57 GB at 4.4 TB/s; 4111 tokens on 8 experts of
 // 4096 x 4096 (top-2) 282 us, 0.98 PFLOP/s; weight gradients of 128 experts in fp32
 // 277-306 us, 1.67 GB at 5.5-6.0 TB/s, of 8 experts of 2048 x 1536 61 us, 0.85 PFLOP/s.
 #include "block_common.h"
@@ -210,17 +210,17 @@ struct Tile {
 // reads.
 template <int W>
 struct Turned {
-  static constexpr int CPR = W / 8;        // 16-byte chunks per row
-  static constexpr int RPC = 64 / CPR;     // rows per copy of a wave
-  __device__ static inline int row(int t, int lane) { return t * RPC + lane / CPR; }
+  static constexpr int CPR = W / 8;  // 16-byte chunks per row
+  static_assert(W % 128 == 0, "rows start in the same bank");
+  __device__ static inline int row(int t, int lane) { return (t * 64 + lane) / CPR; }
   // Column (in values) that the lane's chunk of copy t holds.
   __device__ static inline int col(int t, int lane) {
-    return 8 * ((lane % CPR) ^ (4 * (row(t, lane) & 3) & (CPR - 1)));
+    return 8 * ((t * 64 + lane) % CPR ^ 4 * (row(t, lane) & 3));
   }
   // Byte offset of the lane's first four values of K in sub-tile `sub`, K 0.
   __device__ static inline int off(int sub, int lane) {
     const int i = lane & 15, g = lane >> 4;
-    const int unit = (2 * sub + (g & 1)) ^ (2 * (i >> 2) & (W / 16 - 1));
+    const int unit = (2 * sub + (g & 1)) ^ 2 * (i >> 2);
     return (8 * (g >> 1) + (i >> 2)) * 2 * W + unit * 32 + (i & 3) * 8;
   }
   // Values 16 s + 8 h .. + 7 of K (h the lane's half) at the offset.
@@ -237,7 +237,15 @@ template <int V>
 struct Int {
   static constexpr int value = V;
 };
-constexpr int least(int a, int b) { return a < b ? a : b; }
+// The largest divisor of n that is at most b.
+constexpr int part_of(int n, int b) { return n <= b ? n : n % b == 0 ? b : part_of(n, b - 1); }
+
+template <int N>
+constexpr int largest(const int (&v)[N]) {
+  int m = v[0];
+  for (int i = 1; i < N; i++) m = v[i] > m ? v[i] : m;
+  return m;
+}
 
 // The time of a K block in stage st: the wave issues the matrix instructions of
 // the step before (the last one's of the block before at first; FIRST: there is
@@ -302,33 +310,71 @@ __device__ inline void k_loop(uint8_t* lds, int KB, const Copy& copy, const Read
 }
 
 // 32 rows x 8 NQ columns of a wave's sums (NQ at most ROW bytes of them), turned
-// over in LDS so that consecutive lanes hold consecutive bytes of a row.  The
-// 16-byte pieces of a row lie in an order that changes from row to row (every row
-// where 128 bytes or more make a row, every fourth of 64 bytes), against bank
-// conflicts.  value(q, r): the lane's value of column 8 q + 4 h + r, h its half;
+// over in LDS, ROWS rows at a time, so that consecutive lanes hold consecutive bytes
+// of a row.  The 16-byte pieces of a row lie in an order that changes from row to row
+// (every row where 128 bytes or more make a row, every fourth of 64 bytes), against
+// bank conflicts.  value(q, r): the lane's value of column 8 q + 4 h + r, h its half;
 // then piece(u, byte, address) for 16 bytes of row u * 64 / (ROW / 16) + lane / (ROW
 // / 16).
-template <int NQ, bool F32, int ROW, class Value, class Piece>
+template <int NQ, bool F32, int ROW, int ROWS, class Value, class Piece>
 __device__ inline void turn_over(uint8_t* mine, const Value& value, const Piece& piece) {
   constexpr int EB = F32 ? 4 : 2, PIECES = ROW / 16, RPI = 64 / PIECES;
   static_assert(NQ * 8 * EB <= ROW, "a row's bytes");
   const int lane = threadIdx.x & 63, r32 = lane & 31, h = lane >> 5;
-  static_assert(ROW >= 64, "four pieces");
+  static_assert(ROW >= 64 && ROWS % RPI == 0, "four pieces, whole turns");
   auto order = [](int row) { return (ROW >= 128 ? row : row >> 2) & 7 & (PIECES - 1); };
+  float v[NQ][4];
 #pragma unroll
-  for (int q = 0; q < NQ; q++) {
-    const int byte = (8 * q + 4 * h) * EB;
-    uint8_t* d = mine + r32 * ROW + ((byte / 16) ^ order(r32)) * 16 + byte % 16;
-    const float v[4] = {value(q, 0), value(q, 1), value(q, 2), value(q, 3)};
-    store4<F32>(d, 0, v);
-  }
-  __builtin_amdgcn_wave_barrier();
+  for (int q = 0; q < NQ; q++)
 #pragma unroll
-  for (int u = 0; u < 32 / RPI; u++) {
-    const int row = u * RPI + lane / PIECES, at = lane % PIECES;
-    if (at * 16 < NQ * 8 * EB) piece(u, at * 16, mine + row * ROW + (at ^ order(row)) * 16);
+    for (int r = 0; r < 4; r++) v[q][r] = value(q, r);
+#pragma unroll
+  for (int part = 0; part < 32 / ROWS; part++) {
+    if (ROWS == 32 || r32 / ROWS == part) {
+#pragma unroll
+      for (int q = 0; q < NQ; q++) {
+        const int byte = (8 * q + 4 * h) * EB;
+        uint8_t* d = mine + r32 % ROWS * ROW + ((byte / 16) ^ order(r32)) * 16 + byte % 16;
+        store4<F32>(d, 0, v[q]);
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int u = part * ROWS / RPI; u < (part + 1) * ROWS / RPI; u++) {
+      const int row = u * RPI + lane / PIECES, at = lane % PIECES;
+      if (at * 16 < NQ * 8 * EB)
+        piece(u, at * 16, mine + row % ROWS * ROW + (at ^ order(row)) * 16);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
-  __builtin_amdgcn_wave_barrier();
+}
+
+// LDS of a tile: the stages, room where each wave turns its sums over, ROWS rows x ROW
+// bytes at a time, and the pairs of two tiles; kOffsets more for expert_offsets.
+constexpr int kOffsets = 1028;
+template <class C, int ACT, bool F32>
+struct Room {
+  static constexpr bool WIDE = F32 || ACT == kSiluGrad;  // in fp32 (the gradient: rounded behind)
+  static constexpr int PAIRS = 2 * C::BM * 4;
+  static constexpr int LEFT =
+      (160 * 1024 - C::STAGES * C::STAGE - PAIRS - kOffsets * 4) / C::WAVES;
+  static constexpr int ROWS = LEFT < 2048 ? 8 : 32;
+  static constexpr int ROW =
+      ROWS == 32 && (LEFT < 4096 || (ACT == kSilu && !F32 && C::SN < 4)) ? 64 : 128;
+  static constexpr int BYTES = C::STAGES * C::STAGE + C::WAVES * ROWS * ROW + PAIRS;
+  static_assert(ROWS * ROW <= LEFT, "LDS");
+};
+
+// expert_offsets in LDS (a look-up in memory would wait behind the stores of a tile).
+struct List {
+  const int32_t* expert_offsets;
+  int E;
+};
+
+// Column tiles (with SiLU * mul, N is gate and up together, and so is BN).
+template <class C>
+__host__ __device__ inline int columns(int N) {
+  return (N + C::BN - 1) / C::BN;
 }
 
 // out of every expert.  TRANS: b is [E,K,N] (turned).
@@ -340,24 +386,23 @@ __device__ inline void turn_over(uint8_t* mine, const Value& value, const Piece&
 // 1536 x 512 69 and 64, 2048 x 768 114 and 107, 1536 x 2048 235 and 232).  Stores
 // go past the L2, which the operands' rows need (that product 212 us so).
 //
+// Of several tiles (MORE) the block takes the one whose rounds over the chip cost least
+// for the rows that each expert has: a router that spreads its rows unevenly fills other
+// tiles than one that does not, and the host does not know.
+//
 // Bound (Big at that product, us): its copies alone take 165, with the stores 190;
 // the matrix cores are busy a quarter of the time and add 25.  At 4096^3 they are
 // busy 63% of the time, at the 1.8 GHz that the power leaves.
 template <class C, bool TRANS, int ACT, bool F32>
-__global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(GroupedArgs g) {
+__device__ inline void grouped_tiles(const GroupedArgs& g, const List& list, uint8_t* lds) {
   constexpr int SM = C::SM, SN = C::SN;
   static_assert(C::STAGES == 2 && C::STEPS == 4, "two stages of 64 values");
-  static_assert(ACT != kSilu || (!TRANS && SN % 2 == 0), "a projection, 32 columns of out");
+  static_assert(ACT != kSilu || !TRANS, "a projection");
   static_assert(ACT != kSiluGrad || TRANS, "the gradient's way back");
   static_assert(C::BM <= C::THREADS, "a thread per row");
-  // Sums are turned over 32 rows x ROW bytes at a time, 128 where that fits into LDS.
-  constexpr bool WIDE = F32 || ACT == kSiluGrad;  // in fp32 (the gradient's are rounded behind)
-  constexpr int STAGED = C::STAGES * C::STAGE, PAIRS = 2 * C::BM * 4 + 1028 * 4;
-  constexpr int ROW = STAGED + C::WAVES * 4096 + PAIRS > 160 * 1024 ||
-                              (ACT == kSilu && !F32 && SN < 4) ? 64 : 128;
-  constexpr int ROOM = 32 * ROW;
-  static_assert(STAGED + C::WAVES * ROOM + PAIRS <= 160 * 1024, "LDS");
-  __shared__ __align__(1024) uint8_t lds[STAGED + C::WAVES * ROOM + PAIRS];
+  typedef Room<C, ACT, F32> Rm;
+  constexpr bool WIDE = Rm::WIDE;
+  constexpr int ROWS = Rm::ROWS, ROW = Rm::ROW, ROOM = ROWS * ROW;
   uint8_t* const turn = lds + C::STAGES * C::STAGE;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -366,18 +411,11 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
   // The tile's pairs, and the next one's.
   int32_t* pairs = reinterpret_cast<int32_t*>(turn + C::WAVES * ROOM);
   int32_t* next_pairs = pairs + C::BM;
-  // expert_offsets (a look-up in memory would wait behind the stores of a tile).
-  struct {
-    int32_t* expert_offsets;
-    int E;
-  } list = {pairs + 2 * C::BM, g.E};
-  for (int e = threadIdx.x; e <= g.E; e += C::THREADS) list.expert_offsets[e] = g.expert_offsets[e];
-  __syncthreads();
   // With SiLU * mul a tile is BN / 2 gate rows of b and the BN / 2 up rows of
   // the same columns, eight of each in turn, so that a lane holds both sums.
   constexpr int TN = ACT == kSilu ? C::BN / 2 : C::BN;
   const int cols = ACT == kSilu ? g.N / 2 : g.N;
-  const int ntn = (cols + TN - 1) / TN, KB = (g.K + 63) / 64;
+  const int ntn = columns<C>(g.N), KB = (g.K + 63) / 64;
   Spans<C::BM> spans;
   const int ntm = spans.count(list);
   // The launch order deals blocks to the XCDs in turn: each XCD's blocks take a
@@ -489,10 +527,10 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
                                       reinterpret_cast<u32x4*>(to + (size_t)p * width));
       };
       if constexpr (ACT == kPlain) {
-        constexpr int Q = least(4 * SN, NQ);
+        constexpr int Q = part_of(4 * SN, NQ);
 #pragma unroll
         for (int q0 = 0; q0 < 4 * SN; q0 += Q)
-          turn_over<Q, F32, ROW>(
+          turn_over<Q, F32, ROW, ROWS>(
               mine, [&](int q, int r) { return sum(q0 + q, r); },
               [&](int u, int byte, const uint8_t* v) {
                 const int n = n0 + wn * SN * 32 + q0 * 8 + byte / EB;
@@ -501,22 +539,22 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
       } else if constexpr (ACT == kSilu) {
         const int nw = n0 + wn * SN * 16;  // the wave's first column of out
         if (g.gu != nullptr) {
-          constexpr int Q = least(2 * SN, ROW / 16);
+          constexpr int Q = part_of(2 * SN, ROW / 16);
 #pragma unroll
           for (int up = 0; up < 2; up++)
 #pragma unroll
             for (int q0 = 0; q0 < 2 * SN; q0 += Q)
-              turn_over<Q, false, ROW>(
+              turn_over<Q, false, ROW, ROWS>(
                   mine, [&](int q, int r) { return sum(2 * (q0 + q) + up, r); },
                   [&](int u, int byte, const uint8_t* v) {
                     const int n = nw + q0 * 8 + byte / 2;
                     put(reinterpret_cast<uint8_t*>(g.gu + up * cols + n), g.N * 2, u, n, v);
                   });
         }
-        constexpr int Q = least(2 * SN, NQ);
+        constexpr int Q = part_of(2 * SN, NQ);
 #pragma unroll
         for (int q0 = 0; q0 < 2 * SN; q0 += Q)
-          turn_over<Q, F32, ROW>(
+          turn_over<Q, F32, ROW, ROWS>(
               mine,
               [&](int q, int r) {
                 return silu_mul(sum(2 * (q0 + q), r), sum(2 * (q0 + q) + 1, r));
@@ -528,7 +566,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
       } else {
 #pragma unroll
         for (int q0 = 0; q0 < 4 * SN; q0 += NQ)
-          turn_over<NQ, true, ROW>(
+          turn_over<NQ, true, ROW, ROWS>(
               mine, [&](int q, int r) { return sum(q0 + q, r); },
               [&](int u, int byte, const uint8_t* v) {
                 const int n = n0 + wn * SN * 32 + q0 * 8 + byte / 4, p = row[u];
@@ -648,6 +686,52 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
   }
 }
 
+// Row tiles of the lane's experts, and what the rounds of `tiles` of them cost.
+template <class C>
+__device__ inline int lanes_tiles(const List& list) {
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < list.E; e += 64)
+    n += (list.expert_offsets[e + 1] - list.expert_offsets[e] + C::BM - 1) / C::BM;
+  return n;
+}
+template <class C>
+__device__ inline int cost(const GroupedArgs& g, int tiles) {
+  const int per_xcd = (tiles * columns<C>(g.N) + 7) / 8, slots = max(g.slots / 8, 1);
+  return (per_xcd + slots - 1) / slots * C::ROUND;
+}
+
+template <bool TRANS, int ACT, bool F32, class C, class... MORE>
+__global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(GroupedArgs g) {
+  constexpr int sizes[] = {Room<C, ACT, F32>::BYTES, Room<MORE, ACT, F32>::BYTES...};
+  constexpr int BYTES = largest(sizes);
+  __shared__ __align__(1024) uint8_t lds[BYTES];
+  __shared__ int32_t offsets[kOffsets];
+  for (int e = threadIdx.x; e <= g.E; e += C::THREADS) offsets[e] = g.expert_offsets[e];
+  __syncthreads();
+  const List list = {offsets, g.E};
+  if constexpr (sizeof...(MORE) == 0) {
+    grouped_tiles<C, TRANS, ACT, F32>(g, list, lds);
+  } else {
+    static_assert(((MORE::THREADS == C::THREADS && MORE::EU == C::EU) && ...), "one launch");
+    int tiles[] = {lanes_tiles<C>(list), lanes_tiles<MORE>(list)...};
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1)
+#pragma unroll
+      for (int& n : tiles) n += __shfl_xor(n, off, 64);
+#pragma unroll
+    for (int& n : tiles) n = __builtin_amdgcn_readfirstlane(n);
+    int i = 0, best = 0, least = cost<C>(g, tiles[0]);
+    auto look = [&](int c) {
+      i++;
+      if (c < least) least = c, best = i;
+    };
+    (look(cost<MORE>(g, tiles[i + 1])), ...);
+    if (best == 0) return grouped_tiles<C, TRANS, ACT, F32>(g, list, lds);
+    i = 0;
+    ((best == ++i ? grouped_tiles<MORE, TRANS, ACT, F32>(g, list, lds) : void()), ...);
+  }
+}
+
 // dw of every expert: BM rows (of dw: columns of dy) x BN columns (of x), both
 // operands turned, K the expert's pairs.  A tile of an expert without pairs is
 // zeros.  Bound: dw's bytes where the experts have few rows (128 experts of 1536 x
@@ -751,7 +835,7 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradA
   uint8_t* const out = reinterpret_cast<uint8_t*>(g.out) + (size_t)e * g.N * g.K * EB;
 #pragma unroll
   for (int s = 0; s < SM; s++)
-    turn_over<4 * SN, F32, ROW>(
+    turn_over<4 * SN, F32, ROW, 32>(
         mine, [&](int q, int r) { return acc[q / 4][s][4 * (q % 4) + r]; },
         [&](int u, int byte, const uint8_t* v) {
           const int n = n0 + (s * C::WM + wm) * 32 + u * RPI + lane / (ROW / 16);
@@ -770,25 +854,38 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradA
         });
 }
 
-typedef Tile<256, 256, 2, 4, 2> Big;
-typedef Tile<192, 256, 2, 4, 2> Wide;
-typedef Tile<128, 256, 2, 4, 2> Mid;
+// ROUND: the cost of a round over the chip (one tile per CU), of 320 for Wide's.
+struct Big : Tile<256, 256, 2, 4, 2> {
+  static constexpr int ROUND = 384;
+};
+struct Broad : Tile<192, 384, 2, 4, 2> {
+  static constexpr int ROUND = 490;
+};
+struct Wide : Tile<192, 256, 2, 4, 2> {
+  static constexpr int ROUND = 320;
+};
+struct Mid : Tile<128, 256, 2, 4, 2> {
+  static constexpr int ROUND = 250;
+};
 typedef Tile<64, 128, 2, 2, 2> Half;
 typedef Tile<32, 128, 1, 2, 2> Low;
 
-template <class C, bool TRANS, int ACT, bool F32>
-hipError_t launch_tile(const GroupedArgs& g, hipStream_t s) {
-  constexpr int TN = ACT == kSilu ? C::BN / 2 : C::BN;
-  const int cols = ACT == kSilu ? g.N / 2 : g.N;
-  // At most one row tile per BM rows and one more per expert.
-  const long long ntm = g.M / C::BM + (g.E < g.P ? g.E : g.P);
-  const long long total = (long long)((cols + TN - 1) / TN) * ntm;
+// At most one row tile per BM rows and one more per expert.
+template <class C>
+long long most_tiles(const GroupedArgs& g) {
+  return columns<C>(g.N) * (long long)(g.M / C::BM + (g.E < g.P ? g.E : g.P));
+}
+
+template <bool TRANS, int ACT, bool F32, class C, class... MORE>
+hipError_t launch_tile(GroupedArgs g, hipStream_t s) {
+  long long total = most_tiles<C>(g);
+  ((total = most_tiles<MORE>(g) > total ? most_tiles<MORE>(g) : total), ...);
   if (total > (1ll << 30)) return hipErrorInvalidValue;
   // As many blocks as run at once, each with every so-many'th tile of its XCD (a K
   // of one block has no second one to look the next tile up under: a block each).
-  const long long most = (long long)device_cu_count() * C::PER_CU;
-  const long long grid = g.K > 64 && total > most ? most : total;
-  hipLaunchKernelGGL((grouped_tile_kernel<C, TRANS, ACT, F32>),
+  g.slots = device_cu_count() * C::PER_CU;
+  const long long grid = g.K > 64 && total > g.slots ? g.slots : total;
+  hipLaunchKernelGGL((grouped_tile_kernel<TRANS, ACT, F32, C, MORE...>),
                      dim3((unsigned)((grid + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
   return hipGetLastError();
 }
@@ -818,9 +915,17 @@ hipError_t launch_rows(const GroupedArgs& g, hipStream_t s) {
 //   back  256 (16)     84     94    111    114    122
 //         1024 (64)   141    137    128    131    144
 //         4000 (250)  349    291    265    252    302
-// Among the three widest the one whose rounds over the chip cost least, a round's cost
-// being its tile's rows + 128; where they leave half of the CUs without a tile, Half
-// (8 experts of 1536 x 2048, top-2, 1024 tokens: 32 against 39, 42 and 53 us).
+// Where the four widest leave half of the CUs without a tile, Half (8 experts of 1536 x
+// 2048, top-2, 1024 tokens: 32 against 39, 42 and 53 us); among them the kernel takes the
+// one whose rounds over the chip cost least.  Rounds and us, Mid / Wide / Big / Broad:
+//   back, 768 columns   1024 (64)   2 123  2 127  2 140  1 100
+//                       2048 (128)  3 194  2 151  2 183  1 127
+//                       the same, uneven (some experts above 192 rows)
+//                                   3 192  2 160         2 208
+//                       3000 (188)  3 198  3 227  2 234  2 223
+//   up                  2048 (128)  5 269  3 203  3 197  2 201
+//   down                2500 (156)  8 162  4 119  4 135  3 150
+//   32 experts, 1536 x 2048, top-4, 2500 (312)  3 94  2 79  2 92  1 70
 // Projections of few rows per expert go to the rows kernel ("up": 16 tokens (mean 1) 96
 // us, 128 (8) 168; Low 140 and 172).
 template <bool TRANS, int ACT, bool F32>
@@ -829,20 +934,11 @@ hipError_t launch(const GroupedArgs& g, hipStream_t s) {
   if constexpr (!TRANS) {
     if (mean <= 8) return launch_rows<ACT, F32>(g, s);
   }
-  if (mean <= 20) return launch_tile<Low, TRANS, ACT, F32>(g, s);
-  if (mean <= 44) return launch_tile<Half, TRANS, ACT, F32>(g, s);
-  const int cus = device_cu_count(), tn = ACT == kSilu ? 128 : 256;
-  const int cols = ACT == kSilu ? g.N / 2 : g.N, ntn = (cols + tn - 1) / tn;
-  auto tiles = [&](int bm) {  // expected, for a router that spreads the rows at random
-    const double of_one = g.E == 1 ? (g.P + bm - 1) / bm : mean / bm + 0.5;
-    return (of_one < 1 ? 1 : of_one) * g.E * ntn;
-  };
-  auto cost = [&](int bm) { return ceil(tiles(bm) / cus) * (bm + 128); };
-  if (tiles(128) < cus / 2) return launch_tile<Half, TRANS, ACT, F32>(g, s);
-  if (cost(256) <= cost(192) && cost(256) <= cost(128))
-    return launch_tile<Big, TRANS, ACT, F32>(g, s);
-  return cost(192) <= cost(128) ? launch_tile<Wide, TRANS, ACT, F32>(g, s)
-                                : launch_tile<Mid, TRANS, ACT, F32>(g, s);
+  if (mean <= 20) return launch_tile<TRANS, ACT, F32, Low>(g, s);
+  const double of_one = g.E == 1 ? ceil(mean / Mid::BM) : fmax(mean / Mid::BM + 0.5, 1.0);
+  const double mids = of_one * g.E * columns<Mid>(g.N);  // expected
+  if (mean <= 44 || mids < device_cu_count() / 2) return launch_tile<TRANS, ACT, F32, Half>(g, s);
+  return launch_tile<TRANS, ACT, F32, Big, Broad, Wide, Mid>(g, s);
 }
 
 // Weight gradients.  Short: three blocks on a CU, one storing while others add; Long:

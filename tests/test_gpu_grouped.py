@@ -65,7 +65,9 @@ SIZES = [(1, 8, 2, 64, 64), (1, 1, 1, 8, 8), (3, 16, 4, 96, 136), (7, 4, 4, 48, 
          (1100, 2, 2, 144, 192), (9, 300, 5, 64, 200),
          # enough tiles for the wide ones and for blocks that take several, K of one and two blocks
          (150, 8, 2, 1040, 200), (700, 16, 2, 4112, 136), (1500, 16, 2, 4112, 72),
-         (2200, 16, 2, 4112, 200), (2200, 16, 2, 2064, 64), (700, 2, 1, 4088, 2040)]
+         (2200, 16, 2, 4112, 200), (2200, 16, 2, 2064, 64), (700, 2, 1, 4088, 2040),
+         (700, 16, 2, 2064, 200), (700, 16, 2, 2064, 72), (1500, 16, 2, 2064, 136),
+         (1000, 16, 2, 4080, 64), (1500, 16, 2, 3080, 72)]
 
 
 @pytest.mark.parametrize("trans", [False, True])
