@@ -695,9 +695,9 @@ __device__ inline int lanes_tiles(const List& list) {
   return n;
 }
 template <class C>
-__device__ inline int cost(const GroupedArgs& g, int tiles) {
+__device__ inline long long cost(const GroupedArgs& g, int tiles) {
   const int per_xcd = (tiles * columns<C>(g.N) + 7) / 8, slots = max(g.slots / 8, 1);
-  return (per_xcd + slots - 1) / slots * C::ROUND;
+  return (long long)((per_xcd + slots - 1) / slots) * C::ROUND;
 }
 
 template <bool TRANS, int ACT, bool F32, class C, class... MORE>
@@ -720,8 +720,9 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
       for (int& n : tiles) n += __shfl_xor(n, off, 64);
 #pragma unroll
     for (int& n : tiles) n = __builtin_amdgcn_readfirstlane(n);
-    int i = 0, best = 0, least = cost<C>(g, tiles[0]);
-    auto look = [&](int c) {
+    int i = 0, best = 0;
+    long long least = cost<C>(g, tiles[0]);
+    auto look = [&](long long c) {
       i++;
       if (c < least) least = c, best = i;
     };
