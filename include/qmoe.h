@@ -493,12 +493,13 @@ qmoe_status qmoe_combine_backward(const void* dout, const void* y_pairs, int32_t
  *   group 32, 64 or 128 (32: an expert's matrix of QMOE_W4A16_G32 in the
  *   canonical layout); QMOE_W4_MXFP4: e2m1, scale e8m0 [N, K/32], group 32.
  * The weights are not rounded: a group's sum is formed over exact codes, in
- *   fp32, and scaled once.
+ *   fp32, and scaled once.  Its error is a fraction of sum |x q|: where q is 0
+ *   a finite x counts nothing, however large.
  * act: QMOE_ACT_NONE, or QMOE_ACT_SILU_MUL: rows 0 .. N/2-1 of the weights are
  *   gates and out [M, N/2] = SiLU(g) * u.  add: [.. as out, in its type], added
  *   before the rounding, or NULL; it may be out.  out bf16 or fp32.
- * x is to be finite and below 2^120: a row of x that holds an infinity or a NaN
- *   gives a row of out that is not finite.
+ * Values of x below 2^120 keep a group's sum in range; an infinity or a NaN in
+ *   a row of x reaches that row of out as the formula has it (0 * inf is NaN).
  * ws: qmoe_w4_matmul_workspace(M, N, K) bytes (0: none needed, ws may be NULL),
  *   256-byte aligned, contents need no initialisation; calls that share it must
  *   be ordered on one stream.  K % group == 0; any M and N; x, codes and scale

@@ -7,10 +7,11 @@
 // fp32 over exact values of q, the scale multiplies it once, in fp32: no weight
 // is rounded.
 //
-// int4 as bf16: with u = q ^ 8 = q + 8 in the four highest mantissa bits of 1.0,
-// the pattern 0x3f80 | u << 3 is 1.5 + q / 16, two per word by one multiplication
-// and one bit operation; -1.5 sum_i x, a matrix product with a constant that the
-// sub-tiles of columns share, turns the sum into that of x q / 16.
+// An int4 code enters as q / 16, exact in bf16: a code of 0 adds nothing, whatever x
+// holds there, and a sum's error is a fraction of sum |x q|.  (The pattern 0x3f80 | (q +
+// 8) << 3 of 1.5 + q / 16 takes 9 instead of 13 instructions for eight codes, but its
+// 1.5 comes off by a product of x with a constant, after both are rounded: an error of 24
+// sum |x| half steps, also where all codes are 0.)
 //
 // Measured (int4 in groups of 32 unless said): 1 x 4096 x 4096 5.1 us, 9.4 MB at 1.8
 // TB/s, bound by the launch, a trip to memory and the joining of the waves; 1 x 65536
@@ -28,8 +29,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 enum { kInt4G32, kInt4G64, kInt4G128, kMxfp4 };
 
-// Eight codes (element i in bits 4 i .. 4 i + 3) as bf16: 1.5 + q / 16 of an
-// int4, the value of an e2m1.
+// Eight codes (element i in bits 4 i .. 4 i + 3) as bf16: q / 16 of an int4, the value
+// of an e2m1.
 template <int FMT>
 __device__ inline bf16x8 widen8(uint32_t v) {
   if constexpr (FMT == kMxfp4) {
@@ -39,14 +40,17 @@ __device__ inline bf16x8 widen8(uint32_t v) {
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, 1.0f, 3);
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
   } else {
-    const uint32_t u = v ^ 0x88888888u;
+    // The conversion takes the low four bits of a byte as q, and gives q / 16 in fp32,
+    // whose lower half is 0.
+    uint32_t o = v >> 4;
+    asm("" : "+v"(o));  // (one shift: the bytes are the conversion's operands)
     u32x4 w;
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-      // byte j times (2^3 + 2^15): its low nibble at bit 3, its high one at 19; bit
-      // function 0xea is a & b | c
-      w[j] = __builtin_amdgcn_bitop3_b32(((u >> (8 * j)) & 0xffu) * 0x8008u, 0x00780078u,
-                                         0x3f803f80u, 0xea);
+    for (int j = 0; j < 4; j++) {
+      const float even = __builtin_amdgcn_cvt_off_f32_i4((int)(v >> (8 * j) & 0xffu));
+      const float odd = __builtin_amdgcn_cvt_off_f32_i4((int)(o >> (8 * j) & 0xffu));
+      w[j] = __builtin_amdgcn_perm(__float_as_uint(odd), __float_as_uint(even), 0x07060302u);
+    }
     return __builtin_bit_cast(bf16x8, w);
   }
 }
@@ -241,8 +245,6 @@ __global__ __launch_bounds__(64 * KS) void w4_rows_kernel(W4Args g) {
   for (int m = 0; m < MS; m++)
 #pragma unroll
     for (int s = 0; s < NS; s++) acc[m][s] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const __bf16 mb = __builtin_bit_cast(__bf16, (uint16_t)0xbfc0);  // -1.5
-  const bf16x8 minus = {mb, mb, mb, mb, mb, mb, mb, mb};
   auto compute = [&](const Step& st, const RawScale (&sc)[NS]) {
     u32x4 c[NS];
 #pragma unroll
@@ -279,22 +281,12 @@ __global__ __launch_bounds__(64 * KS) void w4_rows_kernel(W4Args g) {
     constexpr int BPG = FMT == kInt4G64 ? 2 : FMT == kInt4G128 ? 4 : 1;  // blocks per group
 #pragma unroll
     for (int i0 = 0; i0 < 4; i0 += BPG) {
-      f32x4 z[MS];
-#pragma unroll
-      for (int m = 0; m < MS; m++) {
-        z[m] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (FMT != kMxfp4) {
-#pragma unroll
-          for (int i = i0; i < i0 + BPG; i++)
-            z[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][i], minus, z[m], 0, 0, 0);
-        }
-      }
 #pragma unroll
       for (int s = 0; s < NS; s++) {
         const float f = scale_of<FMT>(sc[s], i0);
         f32x4 t[MS];
 #pragma unroll
-        for (int m = 0; m < MS; m++) t[m] = z[m];
+        for (int m = 0; m < MS; m++) t[m] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = i0; i < i0 + BPG; i++) {
           const bf16x8 w = widen8<FMT>(c[s][i]);
@@ -388,16 +380,16 @@ hipError_t launch_rows(const W4Args& g, hipStream_t s) {
 }
 
 // KS waves x NS sub-tiles, 16 rows (32 where there are more than 16).  One sub-tile
-// gives the most blocks, two or four share x's loads and the product with the
-// constant; us (rows x columns x K, int4 in groups of 32):
+// gives the most blocks, two or four share x's loads; us (rows x columns x K, int4 in
+// groups of 32):
 //                        8x1    8x2    4x4
-//   1 x 4096 x 4096       5.2    6.8   11.4
-//   4 x 12288 x 2048      6.9    7.3    7.9
-//   1 x 32768 x 4096     21.1   20.0   20.5
-//   16 x 4096 x 4096      8.0    9.4   13.2
-//   8 x 8192 x 4096      10.1    8.5   13.6
-//   12 x 12288 x 2048     9.8    9.9    8.5
-//   16 x 32768 x 4096    43.3   34.1   25.4
+//   1 x 4096 x 4096       5.1    7.0   12.4
+//   4 x 12288 x 2048      6.8    7.3    8.2
+//   1 x 32768 x 4096     21.4   20.7   23.2
+//   16 x 4096 x 4096      7.7    9.4   13.5
+//   8 x 8192 x 4096      10.3    8.6   14.2
+//   12 x 12288 x 2048     9.9   10.2    8.5
+//   16 x 32768 x 4096    42.8   34.4   25.8
 template <int FMT>
 hipError_t rows(const W4Args& g, hipStream_t s) {
   const int cols = g.act ? g.N / 2 : g.N, cus = device_cu_count();
@@ -423,10 +415,11 @@ hipError_t rows(const W4Args& g, hipStream_t s) {
 // values 16 h .. 16 h + 15, eight per instruction.
 //
 // Bound: every 32 values of K a lane scales 16 sums per sub-tile and widens 16 codes
-// per column, 443 vector instructions beside 48 matrix ones per K block (int4, groups
-// of 32).  At 2048 x 4096 x 4096 (110 us, 0.63 PFLOP/s) the matrix cores are busy 42%
-// of the time, the vector units 51%: they hardly run at once, whatever the order
-// of the two.  MXFP4 needs no product with the constant: 97 us.
+// per column, 491 vector instructions beside 32 matrix ones per K block (int4, groups
+// of 32).  At 2048 x 4096 x 4096 (105 us, 0.65 PFLOP/s) the matrix cores are busy 29%
+// of the time, the vector units 62%: they hardly run at once, whatever the order
+// of the two.  MXFP4's codes take a third of the instructions to widen: 91 us, 34% and
+// 58%; groups of 128 a quarter of the scalings: 83 us.
 template <int BM_, int BN_, int WM_, int WN_>
 struct W4Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -516,8 +509,6 @@ __global__ __launch_bounds__(C::THREADS, 2) void w4_tile_kernel(W4Args g) {
     for (int i = 0; i < SN; i++)
 #pragma unroll
       for (int r = 0; r < 16; r++) acc[j][i][r] = 0.f;
-  const __bf16 mb = __builtin_bit_cast(__bf16, (uint16_t)0xbfc0);  // -1.5
-  const bf16x8 minus = {mb, mb, mb, mb, mb, mb, mb, mb};
   auto block = [&](const uint8_t* __restrict__ st, uint8_t* __restrict__ nx, int kb,
                    const RawScale (&sc)[SN]) {
 #pragma unroll
@@ -573,23 +564,16 @@ __global__ __launch_bounds__(C::THREADS, 2) void w4_tile_kernel(W4Args g) {
           for (int i = 0; i < SN; i++) f[b & 1][i] = scale_of<FMT>(sc[i], b);
           if (b < 3) read(b + 1);
         }
-        f32x16 z = zero;
-        if constexpr (FMT != kMxfp4) {
-#pragma unroll
-          for (int s = 0; s < 2; s++)
-            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[b % AHEAD][j][s], minus, z, 0, 0, 0);
-        }
 #pragma unroll
         for (int s = 0; s < 2; s++)
 #pragma unroll
           for (int i = 0; i < SN; i++)
             t[q & 1][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                x[b % AHEAD][j][s], w[b % AHEAD][i][s], s == 0 ? z : t[q & 1][i], 0, 0, 0);
+                x[b % AHEAD][j][s], w[b % AHEAD][i][s], s == 0 ? zero : t[q & 1][i], 0, 0, 0);
         if (q > 0) scaled(q - 1);
         if (j == SM - 1 && b < 3) widen(b + 1);
-        constexpr int PRODUCTS = 2 * SN + (FMT == kMxfp4 ? 0 : 2);
 #pragma unroll
-        for (int m = 0; m < PRODUCTS; m++) {
+        for (int m = 0; m < 2 * SN; m++) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
           __builtin_amdgcn_sched_group_barrier(0x002, 10, 0);  // vector instructions
         }
@@ -597,7 +581,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void w4_tile_kernel(W4Args g) {
       }
       scaled(4 * SM - 1);
     } else {
-      f32x16 t[SM][SN], z[SM];
+      f32x16 t[SM][SN];
 #pragma unroll
       for (int b = 0; b < 4; b++) {
         if (b > 0) {
@@ -606,11 +590,8 @@ __global__ __launch_bounds__(C::THREADS, 2) void w4_tile_kernel(W4Args g) {
         }
 #pragma unroll
         for (int j = 0; j < SM; j++) {
-          if (b == 0) z[j] = zero;
 #pragma unroll
           for (int s = 0; s < 2; s++) {
-            z[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[b % AHEAD][j][s], minus, z[j], 0, 0,
-                                                           0);
 #pragma unroll
             for (int i = 0; i < SN; i++)
               t[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
@@ -627,7 +608,7 @@ __global__ __launch_bounds__(C::THREADS, 2) void w4_tile_kernel(W4Args g) {
           const float s = scale_of<FMT>(sc[i], 0);
 #pragma unroll
           for (int r = 0; r < 16; r++)
-            acc[j][i][r] = __builtin_fmaf(t[j][i][r] + z[j][r], s, acc[j][i][r]);
+            acc[j][i][r] = __builtin_fmaf(t[j][i][r], s, acc[j][i][r]);
         }
     }
   };
@@ -747,12 +728,12 @@ __global__ __launch_bounds__(256) void w4_sum_kernel(W4Args g) {
 // tiles leave CUs without work is split along K in up to 8 parts of 4 K blocks or more.
 // us (int4 in groups of 32):
 //                        rows   Half in 1     2     4     8 parts   Wide
-//   32 x 4096 x 4096     12.9        41.2  24.6  16.5  14.2
-//   64 x 4096 x 4096     13.7        41.2  24.9  18.5  16.7
-//   64 x 16384 x 2048    28.6        24.4  21.3  23.1  26.4
-//   128 x 4096 x 4096    25.9        41.5  26.6  21.5  24.3
-//   300 x 4096 x 2048                25.2  28.5                       35.6
-//   2048 x 4096 x 4096              131                              113
+//   32 x 4096 x 4096     13.0        38.8  23.9  16.2  13.9
+//   64 x 4096 x 4096     13.5        38.9  24.5  17.5  16.5
+//   64 x 16384 x 2048    26.3        22.6  21.0  22.6  28.5
+//   128 x 4096 x 4096    24.5        39.1  25.9  20.6  23.6
+//   300 x 4096 x 2048                22.7  27.7                       31.1
+//   2048 x 4096 x 4096              132                              107
 typedef W4Tile<128, 128, 2, 2> Wide;
 typedef W4Tile<64, 128, 2, 2> Half;
 enum { kRows, kHalf, kWide };
