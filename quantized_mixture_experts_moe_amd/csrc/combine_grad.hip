@@ -154,24 +154,43 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g)
 
 }  // namespace
 
-hipError_t launch_combine_backward(const CombineBwdArgs& g, hipStream_t s) {
+hipError_t launch_combine_backward(const CombineBwdArgs& all, hipStream_t s) {
   // A wave's pass covers 512 columns: one wave per token up to there.
 #define QMOE_CALL(WPT, F32)                                                                \
   hipLaunchKernelGGL((combine_backward_kernel<WPT, F32>),                                  \
                      dim3((unsigned)((g.T + 4 / WPT - 1) / (4 / WPT))), dim3(256), 0, s, g)
-  if (g.H <= 512) {
-    if (g.f32)
-      QMOE_CALL(1, true);
-    else
-      QMOE_CALL(1, false);
-  } else {
-    if (g.f32)
-      QMOE_CALL(4, true);
-    else
-      QMOE_CALL(4, false);
+  // A grid holds fewer than 2^32 threads (one with more runs only what is left of their
+  // number behind 32 bits, without an error).
+  constexpr int kTokens = 1 << 22;
+  const size_t row = (size_t)all.H * (all.f32 ? 4 : 2);
+  for (int t0 = 0; t0 < all.T; t0 += kTokens) {
+    CombineBwdArgs g = all;
+    const size_t pairs = (size_t)t0 * g.k, logits = (size_t)t0 * g.E;
+    g.T = all.T - t0 < kTokens ? all.T - t0 : kTokens;
+    g.dout = reinterpret_cast<const uint8_t*>(g.dout) + t0 * row;
+    g.y = reinterpret_cast<const uint8_t*>(g.y) + pairs * row;
+    g.dy = reinterpret_cast<uint8_t*>(g.dy) + pairs * row;
+    g.ids += pairs;
+    g.w += pairs;
+    if (g.dw != nullptr) g.dw += pairs;
+    if (g.dlogits != nullptr) g.dlogits += logits;
+    if (g.add != nullptr) g.add += logits;
+    if (g.H <= 512) {
+      if (g.f32)
+        QMOE_CALL(1, true);
+      else
+        QMOE_CALL(1, false);
+    } else {
+      if (g.f32)
+        QMOE_CALL(4, true);
+      else
+        QMOE_CALL(4, false);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
 #undef QMOE_CALL
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace qmoe
