@@ -478,7 +478,8 @@ qmoe_status qmoe_grouped_wgrad(const uint16_t* dy, const uint16_t* x, int32_t pa
  *     dlogits) is not NULL; fp32 [T,E], written whole.
  * dout, y_pairs and dy are bf16 or fp32 (dtype); sums in fp32 in a fixed order.
  * dtopk_w and dlogits may be NULL.  A pair whose id is outside [0,E) gets dy 0
- * and dtopk_w 0, whatever its y_pairs row holds.  dy may be y_pairs.
+ * and dtopk_w 0 and takes no part in the sum over i, whatever its y_pairs row
+ * and its weight hold.  dy may be y_pairs.
  * k <= 16, H % 8 == 0, E <= 1024; dout, y_pairs and dy 16-byte aligned.     */
 qmoe_status qmoe_combine_backward(const void* dout, const void* y_pairs, int32_t dtype,
                                   const int32_t* topk_ids, const float* topk_w, int32_t T,

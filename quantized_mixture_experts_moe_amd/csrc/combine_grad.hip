@@ -61,7 +61,7 @@ __device__ inline void store_past(void* p, size_t i, const float v[8]) {
 template <int WPT, bool F32>
 __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g) {
   constexpr int TPB = 4 / WPT;  // tokens per block
-  __shared__ float sums[4][kMaxK];
+  __shared__ float sums[4][kMaxK], weights[4][kMaxK];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int t = blockIdx.x * TPB + wave / WPT;
@@ -106,7 +106,10 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g)
       for (int u = 0; u < kGroup; u++) {
         if (j0 + u >= k) continue;
         const float s = wave_sum(dot[u]);
-        if (lane == 0) sums[wave][j0 + u] = s;
+        if (lane == 0) {
+          sums[wave][j0 + u] = s;
+          weights[wave][j0 + u] = in[u] ? w[u] : 0.f;  // a dropped pair's counts nothing
+        }
       }
     }
   }
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g)
     if (j < k) {
 #pragma unroll
       for (int v = 0; v < WPT; v++) dw[j] += sums[first + v][j];
-      mean = __builtin_fmaf(g.w[p0 + j], dw[j], mean);
+      mean = __builtin_fmaf(weights[wave][j], dw[j], mean);
     }
   }
   const int at = (wave % WPT) * 64 + lane;
@@ -137,7 +140,7 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(CombineBwdArgs g)
       dz[j] = 0.f;
       id[j] = -1;
       if (j < k) {
-        dz[j] = g.w[p0 + j] * (dw[j] - mean);
+        dz[j] = weights[wave][j] * (dw[j] - mean);
         id[j] = g.ids[p0 + j];
       }
     }
