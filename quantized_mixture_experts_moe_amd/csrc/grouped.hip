@@ -52,11 +52,22 @@ __device__ inline void store4_past(void* p, size_t i, const float v[4]) {
 }
 
 // SiLU(g) u's gradients for the gradient d of the product.  With t = exp(-|g|)
-// neither the sigmoid nor 1 minus it is a difference.
+// neither the sigmoid nor 1 minus it is a difference; t and the quotient are formed as
+// silu_mul does.  The slope, at most 1.1, goes to the larger of d and u first: d u
+// alone can leave fp32's range where the result does not, and the slope times the
+// smaller one can fall below it.
 __device__ inline void silu_mul_grad(float d, float g, float u, float* dg, float* du) {
-  const float t = expf(-fabsf(g)), r = 1.0f / (1.0f + t);
-  const float s = g >= 0.f ? r : t * r, o = g >= 0.f ? t * r : r;  // (NaN: t is NaN)
-  *dg = d * u * (s * (1.0f + g * o));
+  const float x = fminf(fabsf(g), 1000.0f);  // (a NaN of g is in g's own products below)
+  const float hi = x * -1.44269502162933349609375f;
+  const float lo = __builtin_fmaf(x, -1.44269502162933349609375f, -hi) - x * 1.925963033500e-8f;
+  float t = __builtin_amdgcn_exp2f(hi);
+  t = __builtin_fmaf(t, lo * 0.693147180559945f, t);
+  const float v = 1.0f + t;
+  float r = __builtin_amdgcn_rcpf(v);
+  r = __builtin_fmaf(__builtin_fmaf(-v, r, 1.0f), r, r);
+  const float s = g >= 0.f ? r : t * r, o = g >= 0.f ? t * r : r;
+  const bool more = fabsf(d) > fabsf(u);
+  *dg = (s * (1.0f + g * o)) * (more ? d : u) * (more ? u : d);
   *du = d * (g * s);
 }
 
