@@ -64,6 +64,7 @@ struct GroupedArgs {
   int P, k, block_m, E;
   bool pair_rows;
   int slots;  // blocks that run at once (set at the launch)
+  int first;  // tiles of each XCD's share before the launch's (set there)
 };
 struct WgradArgs {
   const uint16_t* dy;  // [P, N]

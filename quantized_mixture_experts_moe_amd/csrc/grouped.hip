@@ -435,7 +435,7 @@ __device__ inline void grouped_tiles(const GroupedArgs& g, const List& list, uin
   constexpr int kBand = 8;
   const int total = ntn * ntm, per = (total + 7) / 8, stride = gridDim.x / 8;
   const int last = min(total, ((int)(blockIdx.x % 8) + 1) * per);
-  int id = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
+  int id = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8) + g.first;
   if (id >= last) return;  // also past the tiles in use
 
   // A tile: expert e, rows from slot m0 to mend, columns from n0.
@@ -621,7 +621,7 @@ __device__ inline void grouped_tiles(const GroupedArgs& g, const List& list, uin
   };
   second();
   for (;;) {
-    const bool more = id + stride < last;
+    const bool more = KB > 1 && id + stride < last;  // (one block has no second one for it)
     const Where next = more ? find(id + stride) : at;
     const int p = more ? my_pair(next) : -1, n0 = at.n0;
     // The wave's sub-tiles of rows are wm, wm + WM, ...; those behind the last one
@@ -882,6 +882,8 @@ struct Mid : Tile<128, 256, 2, 4, 2> {
 typedef Tile<64, 128, 2, 2, 2> Half;
 typedef Tile<32, 128, 1, 2, 2> Low;
 
+constexpr int kBlocks = 1 << 21;  // of a launch
+
 // At most one row tile per BM rows and one more per expert.
 template <class C>
 long long most_tiles(const GroupedArgs& g) {
@@ -897,9 +899,16 @@ hipError_t launch_tile(GroupedArgs g, hipStream_t s) {
   // of one block has no second one to look the next tile up under: a block each).
   g.slots = device_cu_count() * C::PER_CU;
   const long long grid = g.K > 64 && total > g.slots ? g.slots : total;
-  hipLaunchKernelGGL((grouped_tile_kernel<TRANS, ACT, F32, C, MORE...>),
-                     dim3((unsigned)((grid + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
-  return hipGetLastError();
+  // A grid holds fewer than 2^32 threads.
+  for (long long at = 0; at < grid; at += kBlocks) {
+    const long long n = grid - at < kBlocks ? grid - at : kBlocks;
+    g.first = (int)(at / 8);
+    hipLaunchKernelGGL((grouped_tile_kernel<TRANS, ACT, F32, C, MORE...>),
+                       dim3((unsigned)((n + 7) / 8 * 8)), dim3(C::THREADS), 0, s, g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int ACT, bool F32>
@@ -963,15 +972,27 @@ long long wgrad_tiles(const WgradArgs& g) {
   return (long long)((g.K + C::BN - 1) / C::BN) * ((g.N + C::BM - 1) / C::BM) * g.E;
 }
 template <class C>
-hipError_t launch_wgrad(const WgradArgs& g, hipStream_t s) {
-  const long long total = wgrad_tiles<C>(g);
-  if (total > (1ll << 30)) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((total + 7) / 8 * 8));
-  if (g.out_f32)
-    hipLaunchKernelGGL((grouped_wgrad_kernel<C, true>), grid, dim3(C::THREADS), 0, s, g);
-  else
-    hipLaunchKernelGGL((grouped_wgrad_kernel<C, false>), grid, dim3(C::THREADS), 0, s, g);
-  return hipGetLastError();
+hipError_t launch_wgrad(const WgradArgs& all, hipStream_t s) {
+  // As many experts per launch as a grid holds (one always: its matrix would not fit the
+  // memory).
+  const long long each = wgrad_tiles<C>(all) / all.E;
+  if (each * C::THREADS > 0x7fffffffll * 2) return hipErrorInvalidValue;
+  const int most = each < kBlocks ? (int)(kBlocks / each) : 1;
+  const size_t bytes = (size_t)all.N * all.K * (all.out_f32 ? 4 : 2);
+  for (int e0 = 0; e0 < all.E; e0 += most) {
+    WgradArgs g = all;
+    g.E = all.E - e0 < most ? all.E - e0 : most;
+    g.expert_offsets += e0;
+    g.out = reinterpret_cast<uint8_t*>(g.out) + e0 * bytes;
+    const dim3 grid((unsigned)((each * g.E + 7) / 8 * 8));
+    if (g.out_f32)
+      hipLaunchKernelGGL((grouped_wgrad_kernel<C, true>), grid, dim3(C::THREADS), 0, s, g);
+    else
+      hipLaunchKernelGGL((grouped_wgrad_kernel<C, false>), grid, dim3(C::THREADS), 0, s, g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace

@@ -756,7 +756,7 @@ template <class C, int FMT>
 hipError_t launch_tile(W4Args g, int splits, hipStream_t s) {
   const int cols = g.act ? g.N / 2 : g.N, tn = g.act ? C::BN / 2 : C::BN;
   const long long total = (long long)((cols + tn - 1) / tn) * ((g.M + C::BM - 1) / C::BM);
-  if (total > (1ll << 30)) return hipErrorInvalidValue;
+  if (total >= (1ll << 24)) return hipErrorInvalidValue;  // (2^32 threads; out has 256 GiB)
   const int KB = (g.K + 127) / 128;
   g.splits = splits;
   g.split_kb = (KB + splits - 1) / splits;
