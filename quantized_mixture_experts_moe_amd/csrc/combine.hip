@@ -6,6 +6,7 @@
 // Each thread produces 8 consecutive columns of one token; the k expert rows
 // of a token are adjacent in y_pairs (row = pair id), so a block streams
 // them with 16- or 32-byte loads.
+#include "grid_common.h"
 #include "qmoe_internal.h"
 
 namespace qmoe {
@@ -59,7 +60,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
                                                       float* __restrict__ out_f32) {
   constexpr int KU = F32 ? 8 : 16;
   const int groups = H / 8;
-  const size_t gid = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t gid = block_of_grid() * 256 + threadIdx.x;
   if (gid >= (size_t)T * groups) return;
   const int t = (int)(gid / groups);
   const int c = (int)(gid - (size_t)t * groups) * 8;
@@ -112,7 +113,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const void* __restrict__ y
 hipError_t launch_combine(const void* y, int y_f32, const float* w, int T, int k, int H,
                           uint16_t* out_bf16, float* out_f32, hipStream_t s) {
   const size_t n = (size_t)T * (H / 8);
-  const dim3 grid((unsigned)((n + 255) / 256)), block(256);
+  const dim3 grid = grid_of((long long)((n + 255) / 256)), block(256);
   if (y_f32)
     hipLaunchKernelGGL(combine_kernel<true>, grid, block, 0, s, y, w, T, k, H, out_bf16, out_f32);
   else

@@ -26,6 +26,7 @@
 // its gradients with a gate per value at 4111 x 2048 25 + 4 us (4.0 TB/s in the
 // first launch); before at one row of 4096 3.0 us, which is latency.
 #include "block_common.h"
+#include "grid_common.h"
 
 namespace qmoe {
 
@@ -299,7 +300,7 @@ __global__ __launch_bounds__(S::BLOCK) void pre_norm_kernel(const void* __restri
                                                             int T, int H, NormForm f) {
   __shared__ Lds<S> lds;
   const int tr = threadIdx.x % S::TPR;
-  const size_t row = (size_t)blockIdx.x * S::RPB + threadIdx.x / S::TPR;
+  const size_t row = block_of_grid() * S::RPB + threadIdx.x / S::TPR;
   const bool live = row < (size_t)T;
   float v[S::NV][8], wt[S::NV][8];
   load_row<S, F32>(x, live ? row : (size_t)T - 1, H, tr, v);
@@ -345,7 +346,7 @@ __global__ __launch_bounds__(S::BLOCK) void post_norm_kernel(
     const float* __restrict__ w2, NormForm f) {
   __shared__ Lds<S> lds;
   const int tr = threadIdx.x % S::TPR;
-  const size_t row = (size_t)blockIdx.x * S::RPB + threadIdx.x / S::TPR;
+  const size_t row = block_of_grid() * S::RPB + threadIdx.x / S::TPR;
   const bool live = row < (size_t)T;
   const size_t rd = live ? row : (size_t)T - 1;
   float v[S::NV][8], g[S::NV][8], t[S::NV][8], res[S::NV][8];
@@ -604,8 +605,9 @@ hipError_t pre(const void* x, const float* w, float eps, int T, int H, const Nor
 #define QMOE_CALL(SH)                                                                        \
   {                                                                                          \
     typedef QMOE_UNPAREN SH S;                                                               \
-    hipLaunchKernelGGL((pre_norm_kernel<S, F32>), dim3((T + S::RPB - 1) / S::RPB),           \
-                       dim3(S::BLOCK), 0, s, x, w, eps, T, H, f);                            \
+    const dim3 grid = grid_of(((long long)T + S::RPB - 1) / S::RPB);                         \
+    hipLaunchKernelGGL((pre_norm_kernel<S, F32>), grid, dim3(S::BLOCK), 0, s, x, w, eps, T,  \
+                       H, f);                                                                \
   }
   QMOE_NORM_SHAPES(vec, H, QMOE_CALL)
 #undef QMOE_CALL
@@ -621,9 +623,9 @@ hipError_t post(const PostNormArgs& a, hipStream_t s) {
 #define QMOE_CALL(SH)                                                                        \
   {                                                                                          \
     typedef QMOE_UNPAREN SH S;                                                               \
-    hipLaunchKernelGGL((post_norm_kernel<S, F32, G>), dim3((a.T + S::RPB - 1) / S::RPB),     \
-                       dim3(S::BLOCK), 0, s, a.y, a.x, a.w, gate, a.alpha, a.eps, a.T, a.H,  \
-                       a.out, a.w2, a.f);                                                    \
+    const dim3 grid = grid_of(((long long)a.T + S::RPB - 1) / S::RPB);                       \
+    hipLaunchKernelGGL((post_norm_kernel<S, F32, G>), grid, dim3(S::BLOCK), 0, s, a.y, a.x,  \
+                       a.w, gate, a.alpha, a.eps, a.T, a.H, a.out, a.w2, a.f);               \
   }
   QMOE_NORM_SHAPES(vec, a.H, QMOE_CALL)
 #undef QMOE_CALL
