@@ -4,10 +4,11 @@
 //   dlogits[t, ids[t,j]] += w[t,j] (dw[t,j] - sum_i w[t,i] dw[t,i]).
 // Bound: y is read once and dy written once.  WPT waves take a token: a lane
 // holds eight columns of dout at a time and passes over the token's rows of y,
-// whose products it keeps for the rows of a group of kGroup.  All of a group's rows
-// are loaded before the first is used, past the caches, as dy is stored: 4111 tokens,
-// top-8, 2048 columns in bf16 56 us, 291 MB at 5.2 TB/s, a large copy's rate (88 us
-// with a row's load behind its id and through the caches).  A small batch is one trip
+// whose products it keeps for the rows of a group of kGroup (dout is read once per
+// group).  All of a group's rows are loaded before the first is used, past the caches,
+// as dy is stored: 4111 tokens, top-8, 2048 columns in bf16 50-53 us, 291 MB at 5.5-5.8
+// TB/s, a large copy's rate and more (88 us with a row's load behind its id and through the
+// caches; 58 with the weights loaded again at the end).  A small batch is one trip
 // to memory behind the other: 64 tokens, top-2, 256 columns 5.2 us.
 #include "block_common.h"
 #include "qmoe_internal.h"

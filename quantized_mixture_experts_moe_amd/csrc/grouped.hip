@@ -11,10 +11,12 @@
 // Bounds and measured (the rates of a large copy 5.1, of reads alone 6.2, of a fill
 // 6.9 TB/s, of a large dense bf16 product 1.45 PFLOP/s): 4 tokens on 128 experts of
 // 1536 x 2048 (top-8) 38 us, 183 MB of weights at 4.8 TB/s; 2048 tokens there with
-// SiLU * mul and the gate/up kept 197-214 us, 0.89 GB at 4.2-4.5 TB/s; their way back
-// through the down projection 127-134 us, 0.57 GB at 4.4 TB/s; 4111 tokens on 8 experts of
-// 4096 x 4096 (top-2) 282 us, 0.98 PFLOP/s; weight gradients of 128 experts in fp32
-// 277-306 us, 1.67 GB at 5.5-6.0 TB/s, of 8 experts of 2048 x 1536 61 us, 0.85 PFLOP/s.
+// SiLU * mul and the gate/up kept 192-225 us, 0.89 GB at 4.0-4.6 TB/s; their way back
+// through the down projection 125-133 us, 0.57 GB at 4.3-4.6 TB/s; 4111 tokens on 8 experts
+// of 4096 x 4096 (top-2) 282 us, 0.98 PFLOP/s; weight gradients of 128 experts in fp32
+// 276-310 us, 1.67 GB at 5.4-6.0 TB/s, of 8 experts of 2048 x 1536 60-68 us, 0.76-0.86
+// PFLOP/s.  (The first figure is for calls on changing inputs; the second for the same call
+// again and again, back to back.)
 #include "block_common.h"
 #include "qmoe_internal.h"
 #include "tile_common.h"
@@ -244,10 +246,6 @@ struct Turned {
   }
 };
 
-template <int V>
-struct Int {
-  static constexpr int value = V;
-};
 // The largest divisor of n that is at most b.
 constexpr int part_of(int n, int b) { return n <= b ? n : n % b == 0 ? b : part_of(n, b - 1); }
 
@@ -401,9 +399,11 @@ __host__ __device__ inline int columns(int N) {
 // for the rows that each expert has: a router that spreads its rows unevenly fills other
 // tiles than one that does not, and the host does not know.
 //
-// Bound (Big at that product, us): its copies alone take 165, with the stores 190;
-// the matrix cores are busy a quarter of the time and add 25.  At 4096^3 they are
-// busy 63% of the time, at the 1.8 GHz that the power leaves.
+// Bound (that product with 192 x 256 tiles, back to back, us; all of it 214-225): the
+// copies alone 161, with the stores 184, everything but the stores 188; the matrix cores
+// are busy a quarter of the time.  Its way back (192 x 384; 130-133): copies 93, with the
+// gradient's reads and stores 130, everything but those 94.  At 4096^3 the matrix cores
+// are busy 63% of the time, at the 1.8 GHz that the power leaves.
 template <class C, bool TRANS, int ACT, bool F32>
 __device__ inline void grouped_tiles(const GroupedArgs& g, const List& list, uint8_t* lds) {
   constexpr int SM = C::SM, SN = C::SN;
@@ -747,8 +747,10 @@ __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_tile_kernel(Grouped
 // dw of every expert: BM rows (of dw: columns of dy) x BN columns (of x), both
 // operands turned, K the expert's pairs.  A tile of an expert without pairs is
 // zeros.  Bound: dw's bytes where the experts have few rows (128 experts of 1536 x
-// 2048 in fp32: the stores alone take 263 us past the L2 and 308 through it, all of it
-// 296 and 455 (Big)), the matrix cores where they have many.
+// 2048 in fp32, kernel durations: the stores alone 254-261 us, all of it 251-280; through
+// the L2 an earlier form of 256 x 256 tiles took 455 instead of 375).  Of 8 experts of 2048
+// x 1536 with 1028 rows the waves wait for half of their cycles, for K blocks of 32 rows
+// that are copied one ahead: the matrix cores are busy 38% and LDS 24% of the time.
 template <class C, bool F32>
 __global__ __launch_bounds__(C::THREADS, C::EU) void grouped_wgrad_kernel(WgradArgs g) {
   constexpr int SM = C::SM, SN = C::SN;

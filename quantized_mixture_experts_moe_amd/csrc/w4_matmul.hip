@@ -15,8 +15,8 @@
 //
 // Measured (int4 in groups of 32 unless said): 1 x 4096 x 4096 5.1 us, 9.4 MB at 1.8
 // TB/s, bound by the launch, a trip to memory and the joining of the waves; 1 x 65536
-// x 4096, groups of 128, fp32 out, 32-35 us, 139 MB at 4.0-4.3 TB/s; 1500 x 4096 x 2048
-// with add 50-58 us, 0.43-0.50 PFLOP/s.
+// x 4096, groups of 128, fp32 out, 32-36 us, 139 MB at 3.9-4.3 TB/s; 1500 x 4096 x 2048
+// with add 48-55 us, 0.46-0.52 PFLOP/s.
 #include "block_common.h"
 #include "qmoe_internal.h"
 #include "tile_common.h"
