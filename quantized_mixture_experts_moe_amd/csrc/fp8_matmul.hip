@@ -650,7 +650,9 @@ hipError_t launch_tile(Fp8MatmulArgs g, hipStream_t s, int splits = 1) {
   // Grouped: at most one row tile per BM rows and one more per expert.
   const long long ntm = GROUPED ? g.M / C::BM + (g.E < g.P ? g.E : g.P) : (g.M + C::BM - 1) / C::BM;
   const long long total = (long long)((g.N + C::BN - 1) / C::BN) * ntm;
-  if (total > (1ll << 30)) return hipErrorInvalidValue;
+  // (A grid of 2^32 threads would run without an error, but only what is left of them behind
+  // 32 bits; its operands or out would have more than 128 GiB.)
+  if (total + 8 > (1ll << 32) / C::THREADS) return hipErrorInvalidValue;
   g.split_kb = (g.KB + splits - 1) / splits;  // (a part of `splits` has one K block at least)
   hipLaunchKernelGGL((fp8_matmul_tile_kernel<C, GROUPED, BBLOCK, EXACT, OUT32>),
                      dim3((unsigned)((total + 7) / 8 * 8), splits), dim3(C::THREADS), 0, s, g);
